@@ -117,6 +117,10 @@ typedef struct moe_experts {
   int32_t has_shared;
 } moe_experts_t;
 
+/* element types of an output (nvfp4_kv_read) */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F32 1
+
 /*
  * nvfp4_quantize_act - NVFP4 quantisation of a bf16 matrix (activations, or weights at
  * load time): step A4 of the layer. Source: "Basalt" project page, "All the numbers", list
@@ -301,6 +305,117 @@ moe_status moe_layer_decode(const uint16_t* x_bf16, int32_t T, const float* ts_i
                             void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The attention side of a decoder layer: norm and rotation of queries and keys, a paged
+ * key/value cache in NVFP4, and attention over it. The Basalt pages quote their engine with an
+ * int8 cache ("Basalt" project page, "All the numbers") and define none; this cache uses the
+ * layer's own NVFP4 format.
+ *
+ * moe_kv_cache_t - one layer's cache. Codes and scales as nvfp4_quantize_act writes them, the
+ * blocks of 16 along a head's D elements, with a static tensor scale per key/value head.
+ *   k_codes, v_codes   [n_pages][Hkv][page_size][D/2]
+ *   k_scales, v_scales [n_pages][Hkv][page_size][D/16]
+ *   k_ts, v_ts         float32 [Hkv] (device), or NULL for 1
+ * D is 64, 128 or 256; page_size a power of two in [16, 1024]; n_pages * page_size < 2^31.
+ * Token slot s is row s % page_size of page s / page_size. The four arrays are 16-byte
+ * aligned; int32 and float32 arrays of these calls need 4-byte alignment only.
+ */
+typedef struct moe_kv_cache {
+  int32_t n_pages, page_size, Hkv, D;
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_ts;
+  const float* v_ts;
+} moe_kv_cache_t;
+
+/*
+ * moe_qk_prep_t - norm and rotation of query and key heads.
+ *   q_weight, k_weight  float32 [D] (device): y = x / sqrt(mean(x^2) + eps) * weight for each
+ *                       head of D elements; NULL for no norm of the queries / of the keys
+ *   inv_freq            float32 [rot_dim / 2] (device): pair p of a token at position pos turns
+ *                       by pos * inv_freq[p] radians (scaled frequencies give long contexts)
+ *   rot_dim             the first rot_dim elements of a head are rotated, a multiple of 16 in
+ *                       [0, D]; 0 for no rotation (inv_freq and positions may then be NULL)
+ *   interleaved         0: pairs (p, p + rot_dim/2); else pairs (2p, 2p + 1)
+ *   rot_scale           factor on sine and cosine (1 unless the frequency scaling has one)
+ * Computed in float64, rounded to float32 and then to bf16.
+ */
+typedef struct moe_qk_prep {
+  const float* q_weight;
+  const float* k_weight;
+  double eps;
+  const float* inv_freq;
+  int32_t rot_dim;
+  int32_t interleaved;
+  double rot_scale;
+} moe_qk_prep_t;
+
+/*
+ * moe_qk_norm_rope - norm and rotation in one pass.
+ *   q [T][Hq][D], k [T][Hkv][D] bf16: heads side by side, tokens q_stride / k_stride elements
+ *   apart (a multiple of 8; rows of a fused projection's output). Hq or Hkv may be 0.
+ *   positions int32 [T]; q_out [T][Hq][D], k_out [T][Hkv][D] contiguous bf16, 16-byte aligned.
+ *   An output may be its own input when that is contiguous.
+ */
+moe_status moe_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                            int32_t T, int32_t Hq, int32_t Hkv, int32_t D, const int32_t* positions,
+                            const moe_qk_prep_t* prep, uint16_t* q_out, uint16_t* k_out, void* stream);
+
+/*
+ * nvfp4_kv_append - moe_qk_norm_rope of q and k, with the keys and values quantised into the
+ * cache as they are produced: the cache then holds, bit for bit, what nvfp4_quantize_act with
+ * ts_in = the head's tensor scale gives for the bf16 keys of moe_qk_norm_rope and for v.
+ *   k, v [T][Hkv][D] and q [T][Hq][D] as in moe_qk_norm_rope (Hq = 0: no queries);
+ *   slots int32 [T]: where each token goes. A negative slot leaves the cache alone (padding);
+ *   one past the end does too, and sets the device status to MOE_ERR_INVALID_ARG. The slots of
+ *   one call must differ from each other: two tokens with one slot leave a mixture of both.
+ */
+moe_status nvfp4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                           const uint16_t* v, int64_t v_stride, int32_t T, int32_t Hq,
+                           const int32_t* positions, const int32_t* slots, const moe_qk_prep_t* prep,
+                           const moe_kv_cache_t* cache, uint16_t* q_out, void* stream);
+
+/*
+ * nvfp4_kv_read - cached rows back as numbers: k_out, v_out [n][Hkv][D] (either may be NULL),
+ * bf16 or float32 by out_type (MOE_TYPE_*): (e2m1 * e4m3) * ts in float32, rounded once more
+ * for bf16. slots int32 [n], repeats allowed; a negative slot gives zeros, one past the end
+ * too, and sets the device status to MOE_ERR_INVALID_ARG.
+ */
+moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int64_t n, int32_t out_type,
+                         void* k_out, void* v_out, void* stream);
+
+/*
+ * nvfp4_kv_attention - attention of packed sequences over the cache, from one token per
+ * sequence to whole prompts (whose keys and values nvfp4_kv_append has written before).
+ *   q [T][Hq][D] bf16, tokens q_stride elements apart; Hq a multiple of Hkv: query head i reads
+ *   key head i / (Hq / Hkv). cu_q int32 [n_seqs + 1]: sequence b's queries are tokens
+ *   cu_q[b] .. cu_q[b+1] - 1, none or more; max_q (host): the most that any sequence has.
+ *   ctx_lens int32 [n_seqs]: its keys, its own queries' included when causal; block_table
+ *   int32 [n_seqs][max_pages]: the pages that hold them, in order.
+ *   Query i of n is at position ctx - n + i and sees the keys up to its own position (causal
+ *   != 0) or all of them. out [T][Hq][D] bf16 = softmax(scale q k) v; lse float32 [T][Hq] (may
+ *   be NULL) = log sum exp(scale q k). A query that sees no key gets 0 and -infinity. Tokens
+ *   outside cu_q[0] .. cu_q[n_seqs] are left as they were.
+ *   Keys of a page number outside [0, n_pages) count as masked, and set the device status to
+ *   MOE_ERR_INVALID_ARG; cu_q is read as clamped to [0, T] and ctx_lens to the table.
+ *   The sums, maxima and outputs are float32, the softmax weights rounded to float16 and the
+ *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes; it needs no
+ *   initialisation, and calls that may overlap need one each. Results do not depend on what
+ *   runs beside the call.
+ * Limits: D and page_size as the cache, Hq <= 1024, n_seqs <= 65536, T * Hq < 2^31.
+ */
+moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq, const int32_t* cu_q,
+                              const int32_t* ctx_lens, const int32_t* block_table, int32_t n_seqs,
+                              int32_t max_pages, int32_t max_q, const moe_kv_cache_t* cache, float scale,
+                              int32_t causal, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* Bytes of workspace of nvfp4_kv_attention for calls up to these sizes; 0 for sizes it refuses. */
+size_t nvfp4_kv_attention_workspace(int32_t T, int32_t n_seqs, int32_t max_q, int32_t Hq, int32_t Hkv,
+                                    int32_t D);
+
+/*
  * moe_expert_hist - cumulative routing counts and hot-to-cold ranking (A10). Source:
  * "Basalt" project page, section "Expert tiers" (the busiest experts are kept in VRAM, and
  * the tiers follow the conversation as it shifts) and its FAQ "Can it use a second GPU or
@@ -371,8 +486,9 @@ size_t moe_workspace_size(int32_t op, int64_t T, int32_t d, int32_t E, int32_t k
 
 /* Synchronise `stream` and return the device status word of the current device: MOE_OK,
  * MOE_ERR_TIMEOUT (a bounded device-side wait ran out; the kernel stopped early and its
- * outputs are not valid) or MOE_ERR_WORKSPACE (moe_layer_decode found its workspace marked
- * by an earlier call that gave up). `clear` != 0 resets it afterwards. */
+ * outputs are not valid), MOE_ERR_WORKSPACE (moe_layer_decode found its workspace marked
+ * by an earlier call that gave up) or MOE_ERR_INVALID_ARG (a cache slot or page number on the
+ * device was out of range; see the nvfp4_kv_* calls). `clear` != 0 resets it afterwards. */
 moe_status moe_get_device_status(void* stream, int32_t clear, int32_t* status_out);
 
 /* How long a device-side wait (for a copy, a tensor-core result, another CTA) may last before

@@ -23,7 +23,8 @@ MOE_FFN_ACCUMULATE, MOE_FFN_PER_ASSIGN = 0, 1
 MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL, MOE_PATH_CUDA_CORE = 0, 1, 2, 3
 MOE_OP_LAYER, MOE_OP_ROUTE, MOE_OP_QUANT, MOE_OP_FFN, MOE_OP_LAYER_DECODE = 0, 1, 2, 3, 4
 MOE_OP_FFN_STATIC = 5
-MOE_ERR_TIMEOUT, MOE_ERR_WORKSPACE = 4, 5
+MOE_ERR_INVALID_ARG, MOE_ERR_TIMEOUT, MOE_ERR_WORKSPACE = 1, 4, 5
+MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 DEFAULT_WAIT_LIMIT_NS = 2_000_000_000
 
 # (name, restype, argtypes) of every C export; tests check the header declares the same set
@@ -41,6 +42,12 @@ EXPORTS = {
     "moe_expert_hist": (_I32, [_P, _I32, _P, _P, _I32, _P]),
     "moe_layer_decode": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                 _P, _P, _I32, _P, _SZ, _P]),
+    "moe_qk_norm_rope": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "nvfp4_kv_append": (_I32, [_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P]),
+    "nvfp4_kv_read": (_I32, [_P, _P, _I64, _I32, _P, _P, _P]),
+    "nvfp4_kv_attention": (_I32, [_P, _I64, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _P, ctypes.c_float,
+                                  _I32, _P, _P, _P, _SZ, _P]),
+    "nvfp4_kv_attention_workspace": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "moe_workspace_size": (_SZ, [_I32, _I64, _I32, _I32, _I32, _I32]),
     "moe_get_device_status": (_I32, [_P, _I32, ctypes.POINTER(_I32)]),
     "moe_set_wait_limit_ns": (_I32, [ctypes.c_uint64]),
@@ -325,3 +332,219 @@ def moe_set_l2_persisting(nbytes: int) -> int:
 
 def moe_set_wait_limit_ns(ns: int) -> None:
     _check("moe_set_wait_limit_ns", lib().moe_set_wait_limit_ns(int(ns)))
+
+
+# ------------------------------------------------------------------------- key/value cache
+
+class _CacheC(ctypes.Structure):
+    _fields_ = [("n_pages", _I32), ("page_size", _I32), ("Hkv", _I32), ("D", _I32), ("k_codes", _P),
+                ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("k_ts", _P), ("v_ts", _P)]
+
+
+class _PrepC(ctypes.Structure):
+    _fields_ = [("q_weight", _P), ("k_weight", _P), ("eps", ctypes.c_double), ("inv_freq", _P),
+                ("rot_dim", _I32), ("interleaved", _I32), ("rot_scale", ctypes.c_double)]
+
+
+def _need(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Optional[int]:
+    """The device pointer of a contiguous tensor of this type and shape (None in, None out)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _head_rows(t: torch.Tensor, name: str, T: int, D: int, device):
+    """Pointer and token stride of bf16 rows [T][heads][D] whose heads lie side by side."""
+    if t.dtype not in (torch.bfloat16, torch.int16) or t.dim() != 3 or t.device != device:
+        raise ValueError(f"{name} must be a bf16 tensor [T][heads][D] on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    n, heads, d = t.shape
+    s = t.stride()
+    if n != T or d != D or (d > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name} must be [{T}][heads][{D}] with contiguous heads, got {tuple(t.shape)} "
+                         f"with strides {s}")
+    return t.data_ptr(), (s[0] if n > 1 else heads * D)
+
+
+class _On:
+    """The tensors' device as the current one for a call, and the stream to use on it."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+@dataclass(frozen=True)
+class KVCache:
+    """A paged NVFP4 key/value cache of one layer (see moe_kv_cache_t in include/moe_nvfp4.h).
+
+    Token slot s is row s % page_size of page s // page_size."""
+    k_codes: torch.Tensor   # uint8 [n_pages][Hkv][page_size][D/2]
+    k_scales: torch.Tensor  # uint8 [n_pages][Hkv][page_size][D/16]
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+    k_ts: Optional[torch.Tensor] = None  # float32 [Hkv]: static tensor scales (None: 1)
+    v_ts: Optional[torch.Tensor] = None
+    _c: _CacheC = field(default=None, repr=False, compare=False)
+
+    def __post_init__(self):
+        if self.k_codes.dim() != 4:
+            raise ValueError("k_codes must be [n_pages][Hkv][page_size][D/2]")
+        n, H, ps, dh = self.k_codes.shape
+        dev, u8 = self.k_codes.device, torch.uint8
+        p = [_need(self.k_codes, "k_codes", u8, (n, H, ps, dh), dev),
+             _need(self.k_scales, "k_scales", u8, (n, H, ps, dh // 8), dev),
+             _need(self.v_codes, "v_codes", u8, (n, H, ps, dh), dev),
+             _need(self.v_scales, "v_scales", u8, (n, H, ps, dh // 8), dev),
+             _need(self.k_ts, "k_ts", torch.float32, (H,), dev), _need(self.v_ts, "v_ts", torch.float32, (H,), dev)]
+        object.__setattr__(self, "_c", _CacheC(n, ps, H, 2 * dh, *p))
+
+    @classmethod
+    def allocate(cls, n_pages: int, page_size: int, Hkv: int, D: int, k_ts=None, v_ts=None, device="cuda"):
+        """An empty cache (all codes and scales zero)."""
+        def z(n):
+            return torch.zeros(n_pages, Hkv, page_size, n, dtype=torch.uint8, device=device)
+        return cls(z(D // 2), z(D // 16), z(D // 2), z(D // 16), k_ts, v_ts)
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+    @property
+    def D(self):
+        return self._c.D
+
+    @property
+    def Hkv(self):
+        return self._c.Hkv
+
+    @property
+    def page_size(self):
+        return self._c.page_size
+
+    @property
+    def n_pages(self):
+        return self._c.n_pages
+
+
+@dataclass(frozen=True)
+class QKPrep:
+    """Norm and rotation of query and key heads (see moe_qk_prep_t): weights None for no norm,
+    inv_freq None for no rotation."""
+    q_weight: Optional[torch.Tensor] = None  # float32 [D]
+    k_weight: Optional[torch.Tensor] = None  # float32 [D]
+    eps: float = 1e-6
+    inv_freq: Optional[torch.Tensor] = None  # float32 [rot_dim / 2]
+    interleaved: bool = False
+    rot_scale: float = 1.0
+
+    def struct(self, D: int, device) -> _PrepC:
+        f32 = torch.float32
+        half = 0 if self.inv_freq is None else self.inv_freq.numel()
+        return _PrepC(_need(self.q_weight, "q_weight", f32, (D,), device), _need(self.k_weight, "k_weight", f32, (D,), device),
+                      self.eps, _need(self.inv_freq, "inv_freq", f32, (half,), device), 2 * half,
+                      1 if self.interleaved else 0, self.rot_scale)
+
+
+def moe_qk_norm_rope(q, k, positions, prep: QKPrep, q_out, k_out, stream=None):
+    """Norm and rotation of q [T][Hq][D] and k [T][Hkv][D] (either may be None) into contiguous
+    outputs; positions int32 [T]."""
+    x = q if q is not None else k
+    if x is None or x.dim() != 3:
+        raise ValueError("q or k must be given, as [T][heads][D]")
+    T, _, D = x.shape
+    dev = x.device
+    qp, qs = (None, 0) if q is None else _head_rows(q, "q", T, D, dev)
+    kp, ks = (None, 0) if k is None else _head_rows(k, "k", T, D, dev)
+    Hq, Hkv = (0 if q is None else q.shape[1]), (0 if k is None else k.shape[1])
+    qo = None if q is None else _need(q_out, "q_out", q.dtype, (T, Hq, D), dev)
+    ko = None if k is None else _need(k_out, "k_out", k.dtype, (T, Hkv, D), dev)
+    pos = _need(positions, "positions", torch.int32, (T,), dev)
+    c = prep.struct(D, dev)
+    with _On(dev, stream) as s:
+        _check("moe_qk_norm_rope", lib().moe_qk_norm_rope(qp, qs, kp, ks, T, Hq, Hkv, D, pos, ctypes.byref(c), qo, ko, s))
+
+
+def nvfp4_kv_append(q, k, v, positions, slots, prep: QKPrep, cache: KVCache, q_out, stream=None):
+    """Norm and rotation of q and k, and k and v quantised into the cache at slots int32 [T]; q
+    (with q_out) may be None."""
+    if k.dim() != 3:
+        raise ValueError("k must be [T][Hkv][D]")
+    T, Hkv, D = k.shape
+    dev = cache.device
+    if (Hkv, D) != (cache.Hkv, cache.D) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [T][{cache.Hkv}][{cache.D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    Hq = 0 if q is None else q.shape[1]
+    qp, qs = (None, 0) if q is None else _head_rows(q, "q", T, D, dev)
+    kp, ks = _head_rows(k, "k", T, D, dev)
+    vp, vs = _head_rows(v, "v", T, D, dev)
+    qo = None if q is None else _need(q_out, "q_out", q.dtype, (T, Hq, D), dev)
+    pos = _need(positions, "positions", torch.int32, (T,), dev)
+    sl = _need(slots, "slots", torch.int32, (T,), dev)
+    c = prep.struct(D, dev)
+    with _On(dev, stream) as s:
+        _check("nvfp4_kv_append", lib().nvfp4_kv_append(
+            qp, qs, kp, ks, vp, vs, T, Hq, pos, sl, ctypes.byref(c), ctypes.byref(cache._c), qo, s))
+
+
+def nvfp4_kv_read(cache: KVCache, slots, k_out, v_out, stream=None):
+    """Cached rows at slots int32 [n] into k_out and v_out [n][Hkv][D] (bf16 or float32, either
+    may be None); a negative slot gives zeros."""
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        raise ValueError("k_out or v_out must be given")
+    n, dev = slots.numel(), cache.device
+    if out.dtype not in (torch.bfloat16, torch.int16, torch.float32):
+        raise ValueError("k_out and v_out must be bf16 or float32")
+    shape = (n, cache.Hkv, cache.D)
+    ko, vo = _need(k_out, "k_out", out.dtype, shape, dev), _need(v_out, "v_out", out.dtype, shape, dev)
+    sl = _need(slots, "slots", torch.int32, (n,), dev)
+    with _On(dev, stream) as s:
+        _check("nvfp4_kv_read", lib().nvfp4_kv_read(
+            ctypes.byref(cache._c), sl, n, MOE_TYPE_F32 if out.dtype is torch.float32 else MOE_TYPE_BF16, ko, vo, s))
+
+
+def nvfp4_kv_attention_workspace(T: int, n_seqs: int, max_q: int, Hq: int, cache: KVCache) -> int:
+    """Bytes of workspace of nvfp4_kv_attention for calls up to these sizes."""
+    return int(lib().nvfp4_kv_attention_workspace(T, n_seqs, max_q, Hq, cache.Hkv, cache.D))
+
+
+def nvfp4_kv_attention(q, cu_q, ctx_lens, block_table, max_q: int, cache: KVCache, scale: float, causal: bool, out,
+                       lse, ws, stream=None):
+    """Attention of packed queries q [T][Hq][D] over the cache (see include/moe_nvfp4.h): sequence
+    b's queries are rows cu_q[b] .. cu_q[b+1]-1 (at most max_q), its keys the ctx_lens[b] tokens
+    of the pages block_table[b]. lse float32 [T][Hq] may be None."""
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [T][Hq][D] and block_table [n_seqs][max_pages]")
+    T, Hq, D = q.shape
+    if D != cache.D:
+        raise ValueError(f"q has heads of {D}, the cache of {cache.D}")
+    dev, i32 = cache.device, torch.int32
+    n, pages = block_table.shape
+    qp, qs = _head_rows(q, "q", T, D, dev)
+    cu, ctx = _need(cu_q, "cu_q", i32, (n + 1,), dev), _need(ctx_lens, "ctx_lens", i32, (n,), dev)
+    table = _need(block_table, "block_table", i32, (n, pages), dev)
+    o, e = _need(out, "out", q.dtype, (T, Hq, D), dev), _need(lse, "lse", torch.float32, (T, Hq), dev)
+    if ws is None or ws.device != dev:
+        raise ValueError(f"ws must be on {dev}")
+    with _On(dev, stream) as s:
+        _check("nvfp4_kv_attention", lib().nvfp4_kv_attention(
+            qp, qs, T, Hq, cu, ctx, table, n, pages, max_q, ctypes.byref(cache._c), scale, 1 if causal else 0, o, e,
+            _ptr(ws), ws.numel() * ws.element_size(), s))

@@ -28,6 +28,7 @@ moe_status cuda_fail(cudaError_t e, const char* where) {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSms = 160;  // workspace sizes asked for without a device cover this many
 struct DeviceInfo {
   bool ready = false;
   int num_sms = 0;
@@ -114,6 +115,75 @@ moe_status check_weights(const moe_expert_weights_t& w, const char* name, int E,
 ExpertGroup to_group(const moe_expert_weights_t& w) {
   return ExpertGroup{w.gu_codes, w.gu_scales,   w.gu_ts,       w.dn_codes, w.dn_scales, w.dn_ts,
                      w.gu_sf_tiled, w.dn_sf_tiled, w.dec_pack, w.hot_pack, w.hot_slot, w.n_hot};
+}
+
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+moe_status check_cache(const moe_kv_cache_t* c) {
+  if (!c) return fail(MOE_ERR_INVALID_ARG, "null cache");
+  if (c->n_pages < 1 || c->Hkv < 1) return fail(MOE_ERR_INVALID_ARG, "the cache needs n_pages >= 1 and Hkv >= 1");
+  if (c->D != 64 && c->D != 128 && c->D != 256) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "D must be 64, 128 or 256");
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "page_size must be a power of two in [16, 1024]");
+  if ((int64_t)c->n_pages * c->page_size > 0x7fffffff || c->Hkv > 1024)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "the cache holds at most 2^31 - 1 tokens of at most 1024 heads");
+  const void* p[4] = {c->k_codes, c->k_scales, c->v_codes, c->v_scales};
+  for (const void* v : p) {
+    if (!v) return fail(MOE_ERR_INVALID_ARG, "null cache pointer");
+    if (!aligned16(v)) return fail(MOE_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  }
+  if (!aligned4(c->k_ts) || !aligned4(c->v_ts)) return fail(MOE_ERR_INVALID_ARG, "k_ts and v_ts must be 4-byte aligned");
+  return MOE_OK;
+}
+
+KvCacheArgs to_cache(const moe_kv_cache_t& c) {
+  return KvCacheArgs{c.n_pages, c.page_size, c.Hkv, c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_ts, c.v_ts};
+}
+
+// Rows of `heads` heads of D bf16 elements, `stride` elements apart.
+moe_status check_rows(const uint16_t* x, int64_t stride, int heads, int D, const char* name) {
+  const std::string n(name);
+  if (!x) return fail(MOE_ERR_INVALID_ARG, "null " + n);
+  if (!aligned16(x)) return fail(MOE_ERR_INVALID_ARG, n + " must be 16-byte aligned");
+  if (stride < (int64_t)heads * D || stride % 8)
+    return fail(MOE_ERR_INVALID_ARG, n + "_stride must be a multiple of 8 and at least the token's heads * D");
+  return MOE_OK;
+}
+
+moe_status check_prep(const moe_qk_prep_t* p, int D, const int32_t* positions) {
+  if (!p) return fail(MOE_ERR_INVALID_ARG, "null prep");
+  if (p->rot_dim < 0 || p->rot_dim > D || p->rot_dim % 16)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rot_dim must be a multiple of 16 in [0, D]");
+  if (p->rot_dim > 0 && (!positions || !p->inv_freq))
+    return fail(MOE_ERR_INVALID_ARG, "a rotation needs positions and inv_freq");
+  if (!(p->eps >= 0.0)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!aligned4(positions) || !aligned4(p->inv_freq) || !aligned4(p->q_weight) || !aligned4(p->k_weight))
+    return fail(MOE_ERR_INVALID_ARG, "positions, inv_freq and the weights must be 4-byte aligned");
+  return MOE_OK;
+}
+
+void set_prep(QkvPrepArgs* a, const moe_qk_prep_t& p, const int32_t* positions) {
+  a->q_weight = p.q_weight;
+  a->k_weight = p.k_weight;
+  a->eps = p.eps;
+  a->positions = positions;
+  a->inv_freq = p.inv_freq;
+  a->rot = p.rot_dim;
+  a->interleaved = p.interleaved ? 1 : 0;
+  a->rot_scale = p.rot_scale;
+}
+
+// The attention workspace: `meta` of every block, then the partial results.
+struct KvAttnWs {
+  size_t part_stride, meta_bytes, bytes;
+};
+KvAttnWs kv_attn_ws(int sms, int D) {
+  KvAttnWs w;
+  const size_t blocks = (size_t)sms * 2;
+  w.part_stride = kv_attn_dec_part_floats(D);
+  w.meta_bytes = align256(blocks * sizeof(int4));
+  w.bytes = w.meta_bytes + align256(blocks * 2 * w.part_stride * sizeof(float));
+  return w;
 }
 
 }  // namespace
@@ -499,6 +569,150 @@ moe_status moe_hot_tier_update(const moe_expert_weights_t* W, const int32_t* ran
   cudaError_t e = launch_hot_tier(W->dec_pack, rank, W->E, W->d, W->I, n_hot, hot_pack, hot_slot, sms,
                                   (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_hot_tier_update launch");
+}
+
+moe_status moe_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, int32_t T,
+                            int32_t Hq, int32_t Hkv, int32_t D, const int32_t* positions, const moe_qk_prep_t* prep,
+                            uint16_t* q_out, uint16_t* k_out, void* stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0) return fail(MOE_ERR_INVALID_ARG, "T, Hq and Hkv must be >= 0");
+  if (D != 64 && D != 128 && D != 256) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "D must be 64, 128 or 256");
+  if (Hq > 1024 || Hkv > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "at most 1024 heads");
+  moe_status s = check_prep(prep, D, T > 0 ? positions : prep ? reinterpret_cast<const int32_t*>(prep->inv_freq) : nullptr);
+  if (s != MOE_OK) return s;
+  if (T == 0 || Hq + Hkv == 0) return MOE_OK;
+  if (Hq > 0 && (s = check_rows(q, q_stride, Hq, D, "q")) != MOE_OK) return s;
+  if (Hkv > 0 && (s = check_rows(k, k_stride, Hkv, D, "k")) != MOE_OK) return s;
+  if ((Hq > 0 && !q_out) || (Hkv > 0 && !k_out)) return fail(MOE_ERR_INVALID_ARG, "null output");
+  if (!aligned16(q_out) || !aligned16(k_out)) return fail(MOE_ERR_INVALID_ARG, "q_out and k_out must be 16-byte aligned");
+  int sms = 0;
+  int32_t* dstatus = nullptr;
+  if ((s = device_info(&sms, &dstatus)) != MOE_OK) return s;
+  QkvPrepArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hkv;
+  set_prep(&a, *prep, positions);
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.status = dstatus;
+  cudaError_t e = launch_qkv_prep(a, D, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_qk_norm_rope launch");
+}
+
+moe_status nvfp4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                           int64_t v_stride, int32_t T, int32_t Hq, const int32_t* positions, const int32_t* slots,
+                           const moe_qk_prep_t* prep, const moe_kv_cache_t* cache, uint16_t* q_out, void* stream) {
+  if (T < 0 || Hq < 0) return fail(MOE_ERR_INVALID_ARG, "T and Hq must be >= 0");
+  if (Hq > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "at most 1024 heads");
+  moe_status s = check_cache(cache);
+  if (s != MOE_OK) return s;
+  s = check_prep(prep, cache->D, T > 0 ? positions : prep ? reinterpret_cast<const int32_t*>(prep->inv_freq) : nullptr);
+  if (s != MOE_OK) return s;
+  if (T == 0) return MOE_OK;
+  if (Hq > 0 && (s = check_rows(q, q_stride, Hq, cache->D, "q")) != MOE_OK) return s;
+  if ((s = check_rows(k, k_stride, cache->Hkv, cache->D, "k")) != MOE_OK) return s;
+  if ((s = check_rows(v, v_stride, cache->Hkv, cache->D, "v")) != MOE_OK) return s;
+  if (!slots || !aligned4(slots)) return fail(MOE_ERR_INVALID_ARG, "slots must be given, 4-byte aligned");
+  if (Hq > 0 && (!q_out || !aligned16(q_out))) return fail(MOE_ERR_INVALID_ARG, "q_out must be given, 16-byte aligned");
+  int sms = 0;
+  int32_t* dstatus = nullptr;
+  if ((s = device_info(&sms, &dstatus)) != MOE_OK) return s;
+  QkvPrepArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = a.Hv = cache->Hkv;
+  set_prep(&a, *prep, positions);
+  a.slots = slots;
+  a.cache = to_cache(*cache);
+  a.q_out = q_out;
+  a.status = dstatus;
+  cudaError_t e = launch_qkv_prep(a, cache->D, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "nvfp4_kv_append launch");
+}
+
+moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int64_t n, int32_t out_type, void* k_out,
+                         void* v_out, void* stream) {
+  if (n < 0) return fail(MOE_ERR_INVALID_ARG, "n must be >= 0");
+  moe_status s = check_cache(cache);
+  if (s != MOE_OK) return s;
+  if (out_type != MOE_TYPE_BF16 && out_type != MOE_TYPE_F32) return fail(MOE_ERR_INVALID_ARG, "bad out_type");
+  if (n > ((int64_t)1 << 40)) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n is too large");
+  if (n == 0) return MOE_OK;
+  if (!slots || !aligned4(slots)) return fail(MOE_ERR_INVALID_ARG, "slots must be given, 4-byte aligned");
+  if (!k_out && !v_out) return fail(MOE_ERR_INVALID_ARG, "k_out or v_out must be given");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(MOE_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  int sms = 0;
+  int32_t* dstatus = nullptr;
+  if ((s = device_info(&sms, &dstatus)) != MOE_OK) return s;
+  cudaError_t e = launch_kv_read(to_cache(*cache), cache->D, slots, n, k_out, v_out, out_type == MOE_TYPE_F32, dstatus,
+                                 sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "nvfp4_kv_read launch");
+}
+
+size_t nvfp4_kv_attention_workspace(int32_t T, int32_t n_seqs, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (T < 0 || n_seqs < 0 || max_q < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
+  return kv_attn_ws(kMaxSms, D).bytes;
+}
+
+moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq, const int32_t* cu_q,
+                              const int32_t* ctx_lens, const int32_t* block_table, int32_t n_seqs, int32_t max_pages,
+                              int32_t max_q, const moe_kv_cache_t* cache, float scale, int32_t causal, uint16_t* out,
+                              float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || n_seqs < 0 || max_pages < 0 || max_q < 0)
+    return fail(MOE_ERR_INVALID_ARG, "T, n_seqs, max_pages and max_q must be >= 0");
+  moe_status s = check_cache(cache);
+  if (s != MOE_OK) return s;
+  if (Hq < 1 || Hq % cache->Hkv) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "Hq must be a positive multiple of Hkv");
+  if (Hq > 1024 || n_seqs > 65536 || (int64_t)T * Hq > 0x7fffffff)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "at most 1024 heads, 65536 sequences and 2^31 - 1 query rows");
+  if (!(scale == scale)) return fail(MOE_ERR_INVALID_ARG, "scale is NaN");
+  if (T == 0 || n_seqs == 0) return MOE_OK;
+  if (max_q < 1) return fail(MOE_ERR_INVALID_ARG, "max_q must be the longest sequence's query tokens");
+  if ((s = check_rows(q, q_stride, Hq, cache->D, "q")) != MOE_OK) return s;
+  if (!cu_q || !ctx_lens || (max_pages > 0 && !block_table) || !out) return fail(MOE_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned4(cu_q) || !aligned4(ctx_lens) || !aligned4(block_table) || !aligned4(lse))
+    return fail(MOE_ERR_INVALID_ARG, "cu_q, ctx_lens, block_table and lse must be 4-byte aligned");
+  if (!aligned16(out)) return fail(MOE_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  int sms = 0;
+  int32_t* dstatus = nullptr;
+  if ((s = device_info(&sms, &dstatus)) != MOE_OK) return s;
+  const KvAttnWs w = kv_attn_ws(sms, cache->D);
+  if ((s = check_ws(ws, ws_bytes, w.bytes)) != MOE_OK) return s;
+  KvAttnArgs a = {};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.T = T;
+  a.Hq = Hq;
+  a.G = Hq / cache->Hkv;
+  a.cu_q = cu_q;
+  a.ctx_lens = ctx_lens;
+  a.block_table = block_table;
+  a.n_seqs = n_seqs;
+  a.max_pages = max_pages;
+  a.max_q = max_q < T ? max_q : T;
+  a.cache = to_cache(*cache);
+  a.scale = scale;
+  a.causal = causal ? 1 : 0;
+  a.out = out;
+  a.lse = lse;
+  a.meta = reinterpret_cast<int4*>(ws);
+  a.partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + w.meta_bytes);
+  a.part_stride = w.part_stride;
+  a.status = dstatus;
+  for (a.page_shift = 0; (1 << a.page_shift) < cache->page_size;) ++a.page_shift;
+  a.dec_max_rows = 0x7fffffff;
+  cudaError_t e = launch_kv_attn_dec(a, cache->D, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "nvfp4_kv_attention launch");
 }
 
 moe_status moe_set_l2_persisting(size_t bytes, size_t* bytes_out) {

@@ -12,6 +12,7 @@ constexpr int kBlock = 16;          // NVFP4 elements per E4M3 scale
 constexpr float kE2M1Max = 6.0f;
 constexpr float kE4M3Max = 448.0f;
 constexpr int kMaxPartials = 1024;  // per-CTA partial amax values kept in the workspace
+constexpr int32_t kStatusInvalid = 1;  // MOE_ERR_INVALID_ARG: an index read on the device was out of range
 
 // Programmatic dependent launch: let the next kernel on the stream start launching, and
 // wait until the previous kernel's writes are visible (no-ops without the launch attribute).

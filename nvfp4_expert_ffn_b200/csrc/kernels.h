@@ -179,6 +179,61 @@ cudaError_t launch_hot_tier(const uint8_t* dec_pack, const int32_t* rank, int E,
 cudaError_t launch_pack_sf(const ExpertGroup& g, int E, int d, int I, uint8_t* gu_t, uint8_t* dn_t,
                            int num_sms, cudaStream_t st);
 
+// the paged NVFP4 key/value cache (moe_kv_cache_t)
+struct KvCacheArgs {
+  int n_pages, page_size, Hkv;
+  uint8_t* k_codes;   // [n_pages][Hkv][page_size][D/2]
+  uint8_t* k_scales;  // [n_pages][Hkv][page_size][D/16]
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_ts;  // [Hkv] or NULL (1)
+  const float* v_ts;
+};
+
+// norm and rotation of queries and keys, and the quantised write of keys and values
+struct QkvPrepArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int T, Hq, Hk, Hv;                     // Hq, Hk, Hv: head rows taken of each (0: none)
+  const float *q_weight, *k_weight;      // [D] or NULL (no norm)
+  double eps;
+  const int32_t* positions;
+  const float* inv_freq;  // [rot / 2]
+  int rot, interleaved;
+  double rot_scale;
+  const int32_t* slots;  // NULL: nothing is cached
+  KvCacheArgs cache;
+  uint16_t *q_out, *k_out;
+  int32_t* status;
+};
+
+cudaError_t launch_qkv_prep(const QkvPrepArgs& a, int D, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_read(const KvCacheArgs& c, int D, const int32_t* slots, int64_t n, void* k, void* v, bool f32,
+                           int32_t* status, int num_sms, cudaStream_t st);
+
+// attention over the cache
+struct KvAttnArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int T, Hq, G;  // G = Hq / Hkv query heads to a key head
+  const int32_t *cu_q, *ctx_lens, *block_table;
+  int n_seqs, max_pages, max_q, page_shift;
+  KvCacheArgs cache;
+  float scale;
+  int causal;
+  uint16_t* out;
+  float* lse;
+  int dec_max_rows;    // sequences with more query rows per key head are not the decode kernel's
+  float* partial;      // [blocks][2][part_stride]
+  size_t part_stride;  // floats
+  int4* meta;          // [blocks]
+  int32_t* status;
+};
+
+size_t kv_attn_dec_part_floats(int D);
+cudaError_t init_kv_attn_dec_attributes();
+cudaError_t launch_kv_attn_dec(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st);
+
 // the bounded-wait limit of each translation unit with device-side waits, on the current device
 cudaError_t set_wait_limit_ffn_decode(unsigned long long ns);
 cudaError_t set_wait_limit_ffn_tc(unsigned long long ns);
@@ -211,6 +266,8 @@ inline cudaError_t init_kernel_attributes() {
   e = init_ffn_tc_attributes();
   if (e != cudaSuccess) return e;
   e = init_ffn_dec_attributes();
+  if (e != cudaSuccess) return e;
+  e = init_kv_attn_dec_attributes();
   if (e != cudaSuccess) return e;
   return init_layer_dec_attributes();
 }

@@ -1,12 +1,15 @@
-"""One MoE layer forward through the C ABI: buffers on the GPU and the five calls in order.
+"""One decoder layer's two halves through the C ABI: buffers on the GPU and the calls in order.
 
-    quantise x -> route (router, top-k, permutation) -> expert FFN -> combine -> histogram
+    MoeLayer:         quantise x -> route (router, top-k, permutation) -> expert FFN -> combine
+                      -> histogram
+    CachedAttention:  norm, rotation and quantised cache write -> attention over the cache
 
 Each step is one call of libmoe_nvfp4.so; this module only allocates device buffers
 (torch) and passes pointers.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -223,3 +226,51 @@ class GraphedMoeLayer:
         self.run(0)
         self.stream.synchronize()
         y_host.copy_(self.y_host)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0, trained: int = 0,
+                     slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """Frequencies of the rotation and the factor on its sine and cosine, for binding.QKPrep:
+    base^(-2p/rot_dim), p < rot_dim/2, as float32. A `factor` above 1 stretches the positions:
+    all frequencies divided by it (trained = 0), or, given the trained context length, only
+    those that turn at most `slow` times within it, those that turn at least `fast` times kept,
+    a linear ramp between, and a factor 0.1 ln(factor) + 1 on sine and cosine."""
+    f = base ** (-2.0 * torch.arange(rot_dim // 2, dtype=torch.float64) / rot_dim)
+    scale = 1.0
+    if factor > 1.0 and trained == 0:
+        f = f / factor
+    elif factor > 1.0:
+        turns = trained * f / (2.0 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        scale = 0.1 * math.log(factor) + 1.0
+    return f.to(torch.float32).to(device), scale
+
+
+class CachedAttention:
+    """The attention core of one layer over its NVFP4 cache, for up to T_max tokens and
+    n_seqs_max sequences a call: buffers, and the two calls in order. The projections before and
+    after it are the caller's."""
+
+    def __init__(self, cache: B.KVCache, prep: B.QKPrep, Hq: int, T_max: int, n_seqs_max: int,
+                 scale: Optional[float] = None):
+        self.cache, self.prep, self.Hq, self.T_max, self.n_seqs_max = cache, prep, Hq, T_max, n_seqs_max
+        self.scale = cache.D ** -0.5 if scale is None else scale
+        dev = cache.device
+        self.q = torch.empty(T_max, Hq, cache.D, dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(T_max, Hq, cache.D, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(T_max, Hq, dtype=torch.float32, device=dev)
+        n = B.nvfp4_kv_attention_workspace(T_max, n_seqs_max, T_max, Hq, cache)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+
+    def forward(self, q, k, v, positions, slots, cu_q, ctx_lens, block_table, max_q: int, stream=None) -> torch.Tensor:
+        """Writes k, v [T][Hkv][D] to the cache at `slots` and attends q [T][Hq][D] over it,
+        causally; q, k and v may be views of one projection's output. ctx_lens count the tokens
+        just written. Returns out [T][Hq][D] (a view into this layer's buffer). Allocates
+        nothing, so it can be captured in a CUDA graph."""
+        T = k.shape[0]
+        assert T <= self.T_max and ctx_lens.numel() <= self.n_seqs_max
+        B.nvfp4_kv_append(q, k, v, positions, slots, self.prep, self.cache, self.q[:T], stream=stream)
+        B.nvfp4_kv_attention(self.q[:T], cu_q, ctx_lens, block_table, max_q, self.cache, self.scale, True,
+                             self.out[:T], self.lse[:T], self.ws, stream=stream)
+        return self.out[:T]
