@@ -397,8 +397,8 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   != 0) or all of them. out [T][Hq][D] bf16 = softmax(scale q k) v; lse float32 [T][Hq] (may
  *   be NULL) = log sum exp(scale q k). A query that sees no key gets 0 and -infinity. Tokens
  *   outside cu_q[0] .. cu_q[n_seqs] are left as they were.
- *   Keys of a page number outside [0, n_pages) count as masked, and set the device status to
- *   MOE_ERR_INVALID_ARG; cu_q is read as clamped to [0, T] and ctx_lens to the table.
+ *   Rows of a page number outside [0, n_pages) count as zeros, and set the device status to
+ *   MOE_ERR_INVALID_ARG; cu_q (ascending) is read as clamped to [0, T] and ctx_lens to the table.
  *   The sums, maxima and outputs are float32, the softmax weights rounded to float16 and the
  *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes; it needs no
  *   initialisation, and calls that may overlap need one each. Results do not depend on what

@@ -173,16 +173,22 @@ void set_prep(QkvPrepArgs* a, const moe_qk_prep_t& p, const int32_t* positions) 
   a->rot_scale = p.rot_scale;
 }
 
-// The attention workspace: `meta` of every block, then the partial results.
+// The attention workspace: `meta` of every block, the plan and the row tiles of the tensor-core
+// kernel (where some sequence can have that many rows), and the partial results of the kernel
+// that runs (the two run one after the other).
 struct KvAttnWs {
-  size_t part_stride, meta_bytes, bytes;
+  size_t meta, tiles, partial, part_stride, bytes;
+  bool tc;
 };
-KvAttnWs kv_attn_ws(int sms, int D) {
+KvAttnWs kv_attn_ws(int sms, int64_t T, int n_seqs, int64_t max_q, int G, int D) {
   KvAttnWs w;
   const size_t blocks = (size_t)sms * 2;
-  w.part_stride = kv_attn_dec_part_floats(D);
-  w.meta_bytes = align256(blocks * sizeof(int4));
-  w.bytes = w.meta_bytes + align256(blocks * 2 * w.part_stride * sizeof(float));
+  w.tc = max_q * G > kDecMaxRows;
+  w.meta = 0;
+  w.tiles = align256(blocks * sizeof(int4));
+  w.partial = w.tiles + 256 + (w.tc ? align256(kv_attn_tc_tiles_bytes(T, n_seqs, G)) : 0);
+  const size_t dec = blocks * 2 * kv_attn_dec_part_floats(D), tc = (size_t)sms * 2 * kv_attn_tc_part_floats(D);
+  w.bytes = w.partial + align256((w.tc && tc > dec ? tc : dec) * sizeof(float));
   return w;
 }
 
@@ -661,7 +667,7 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
 
 size_t nvfp4_kv_attention_workspace(int32_t T, int32_t n_seqs, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D) {
   if (T < 0 || n_seqs < 0 || max_q < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-  return kv_attn_ws(kMaxSms, D).bytes;
+  return kv_attn_ws(kMaxSms, T, n_seqs, max_q, Hq / Hkv, D).bytes;
 }
 
 moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq, const int32_t* cu_q,
@@ -686,32 +692,42 @@ moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, in
   int sms = 0;
   int32_t* dstatus = nullptr;
   if ((s = device_info(&sms, &dstatus)) != MOE_OK) return s;
-  const KvAttnWs w = kv_attn_ws(sms, cache->D);
+  const int G = Hq / cache->Hkv;
+  max_q = max_q < T ? max_q : T;
+  const KvAttnWs w = kv_attn_ws(sms, T, n_seqs, max_q, G, cache->D);
   if ((s = check_ws(ws, ws_bytes, w.bytes)) != MOE_OK) return s;
   KvAttnArgs a = {};
   a.q = q;
   a.q_stride = q_stride;
   a.T = T;
   a.Hq = Hq;
-  a.G = Hq / cache->Hkv;
+  a.G = G;
   a.cu_q = cu_q;
   a.ctx_lens = ctx_lens;
   a.block_table = block_table;
   a.n_seqs = n_seqs;
   a.max_pages = max_pages;
-  a.max_q = max_q < T ? max_q : T;
+  a.max_q = max_q;
   a.cache = to_cache(*cache);
   a.scale = scale;
   a.causal = causal ? 1 : 0;
   a.out = out;
   a.lse = lse;
-  a.meta = reinterpret_cast<int4*>(ws);
-  a.partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + w.meta_bytes);
-  a.part_stride = w.part_stride;
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  a.meta = reinterpret_cast<int4*>(base + w.meta);
+  a.plan = reinterpret_cast<long long*>(base + w.tiles);
+  a.tiles = base + w.tiles + 256;
+  a.max_tiles = kv_attn_tc_max_tiles(T, n_seqs, G);
+  a.partial = reinterpret_cast<float*>(base + w.partial);
   a.status = dstatus;
   for (a.page_shift = 0; (1 << a.page_shift) < cache->page_size;) ++a.page_shift;
-  a.dec_max_rows = 0x7fffffff;
+  a.dec_max_rows = w.tc ? kDecMaxRows : 0x7fffffff;
+  a.part_stride = kv_attn_dec_part_floats(cache->D);
   cudaError_t e = launch_kv_attn_dec(a, cache->D, sms, (cudaStream_t)stream);
+  if (e == cudaSuccess && w.tc) {
+    a.part_stride = kv_attn_tc_part_floats(cache->D);
+    e = launch_kv_attn_tc(a, cache->D, sms, (cudaStream_t)stream);
+  }
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "nvfp4_kv_attention launch");
 }
 

@@ -227,10 +227,20 @@ struct KvAttnArgs {
   float* partial;      // [blocks][2][part_stride]
   size_t part_stride;  // floats
   int4* meta;          // [blocks]
+  long long* plan;     // [2] of the tensor-core kernel: a head's work, its row tiles
+  void* tiles;         // [max_tiles] row tiles
+  int max_tiles;
   int32_t* status;
 };
 
+constexpr int kDecMaxRows = 32;  // query rows per key head up to which the decode kernel takes a sequence
 size_t kv_attn_dec_part_floats(int D);
+size_t kv_attn_tc_part_floats(int D);
+int kv_attn_tc_max_tiles(int64_t T, int n_seqs, int G);
+size_t kv_attn_tc_tiles_bytes(int64_t T, int n_seqs, int G);
+cudaError_t init_kv_attn_tc_attributes();
+cudaError_t set_wait_limit_kv_attn_tc(unsigned long long ns);
+cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st);
 cudaError_t init_kv_attn_dec_attributes();
 cudaError_t launch_kv_attn_dec(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st);
 
@@ -243,6 +253,7 @@ cudaError_t set_wait_limit_router_tc(unsigned long long ns);
 inline cudaError_t set_wait_limits(unsigned long long ns) {
   cudaError_t e = set_wait_limit_ffn_decode(ns);
   if (e == cudaSuccess) e = set_wait_limit_router_tc(ns);
+  if (e == cudaSuccess) e = set_wait_limit_kv_attn_tc(ns);
   if (e == cudaSuccess) e = set_wait_limit_ffn_tc(ns);
   if (e == cudaSuccess) e = set_wait_limit_ffn_dec(ns);
   if (e == cudaSuccess) e = set_wait_limit_layer_dec(ns);
@@ -268,6 +279,8 @@ inline cudaError_t init_kernel_attributes() {
   e = init_ffn_dec_attributes();
   if (e != cudaSuccess) return e;
   e = init_kv_attn_dec_attributes();
+  if (e != cudaSuccess) return e;
+  e = init_kv_attn_tc_attributes();
   if (e != cudaSuccess) return e;
   return init_layer_dec_attributes();
 }

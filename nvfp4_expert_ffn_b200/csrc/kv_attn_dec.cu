@@ -85,6 +85,14 @@ struct Tile {
   uint32_t k[2][KW], v[4][VW];
   uint32_t ks[2], vs[4];
 
+  MOE_DEV void zero() {  // rows of a page number outside the cache
+#pragma unroll
+    for (int i = 0; i < KW; ++i) k[0][i] = k[1][i] = 0u;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) v[0][i] = v[1][i] = v[2][i] = v[3][i] = 0u;
+    ks[0] = ks[1] = vs[0] = vs[1] = vs[2] = vs[3] = 0u;
+  }
+
   MOE_DEV void load(const KvCacheArgs& c, int64_t row0, int g, int q) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -265,113 +273,116 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
       return ((int64_t)page * a.cache.Hkv + h) * ps + (t0 & (ps - 1));
     };
     int t0 = k0 * kChunk + warp * 16;
-    int page = page_of(t0);
+    const int page = page_of(t0);
     Tile<D> cur, nxt;
-    if (page >= 0) cur.load(a.cache, row_of(page, t0), g, c);
+    if (page >= 0)
+      cur.load(a.cache, row_of(page, t0), g, c);
+    else
+      cur.zero();
     int page_n = page_of(t0 + kDecWarps * 16);
     for (; t0 < tok_end; t0 += kDecWarps * 16) {
       const int t1 = t0 + kDecWarps * 16;
-      if (page_n >= 0) nxt.load(a.cache, row_of(page_n, t1), g, c);
+      if (page_n >= 0)
+        nxt.load(a.cache, row_of(page_n, t1), g, c);
+      else
+        nxt.zero();
       const int page_nn = page_of(t1 + kDecWarps * 16);
-      if (page >= 0) {
-        // S^T = K Q^T
-        float s[NR][4];
+      // S^T = K Q^T
+      float s[NR][4];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
+      for (int r = 0; r < NR; ++r) s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < Tile<D>::KW; ++w) {  // 8 elements of both rows: two k steps
-          uint32_t f0[4], f1[4];
-          e2m1x8_to_f16x2x4(cur.k[0][w], f0);
-          e2m1x8_to_f16x2x4(cur.k[1][w], f1);
-          // the scale of block w / 2 of this quarter in both halves
-          const uint32_t sel = (w / 2) * 0x0011u;
-          const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(cur.ks[0], 0, sel)),
-                         s1 = e4m3x2_to_f16x2(__byte_perm(cur.ks[1], 0, sel));
+      for (int w = 0; w < Tile<D>::KW; ++w) {  // 8 elements of both rows: two k steps
+        uint32_t f0[4], f1[4];
+        e2m1x8_to_f16x2x4(cur.k[0][w], f0);
+        e2m1x8_to_f16x2x4(cur.k[1][w], f1);
+        // the scale of block w / 2 of this quarter in both halves
+        const uint32_t sel = (w / 2) * 0x0011u;
+        const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(cur.ks[0], 0, sel)),
+                       s1 = e4m3x2_to_f16x2(__byte_perm(cur.ks[1], 0, sel));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f0[i] = hmul2(f0[i], s0);
-            f1[i] = hmul2(f1[i], s1);
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t fa[4] = {f0[2 * u], f1[2 * u], f0[2 * u + 1], f1[2 * u + 1]};
-#pragma unroll
-            for (int r = 0; r < NR; ++r) mma_f16(s[r], fa, bq[r][2 * w + u][0], bq[r][2 * w + u][1]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          f0[i] = hmul2(f0[i], s0);
+          f1[i] = hmul2(f1[i], s1);
         }
-        // softmax: columns (query rows) 2c and 2c + 1, keys g and g + 8
-        const bool edge = t0 + 16 > lim_min;
-        uint32_t pb[NR][2];
-        bool raise = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t fa[4] = {f0[2 * u], f1[2 * u], f0[2 * u + 1], f1[2 * u + 1]};
+#pragma unroll
+          for (int r = 0; r < NR; ++r) mma_f16(s[r], fa, bq[r][2 * w + u][0], bq[r][2 * w + u][1]);
+        }
+      }
+      // softmax: columns (query rows) 2c and 2c + 1, keys g and g + 8
+      const bool edge = t0 + 16 > lim_min;
+      uint32_t pb[NR][2];
+      bool raise = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[r][j] *= fac[r][j & 1];
+          if (edge && t0 + g + 8 * (j >> 1) >= lim[r][j & 1]) s[r][j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) raise |= fmaxf(s[r][j], s[r][j + 2]) > m[r][j] + kRaise;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
+          float fix[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[r][j] *= fac[r][j & 1];
-            if (edge && t0 + g + 8 * (j >> 1) >= lim[r][j & 1]) s[r][j] = -INFINITY;
+          for (int j = 0; j < 2; ++j) {
+            float x = fmaxf(s[r][j], s[r][j + 2]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            x = fmaxf(x, m[r][j]);
+            fix[j] = ex2(m[r][j] - x);
+            m[r][j] = x;
+            l[r][j] *= fix[j];
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) raise |= fmaxf(s[r][j], s[r][j + 2]) > m[r][j] + kRaise;
+          for (int i = 0; i < KSTEPS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[r][i][j] *= fix[j & 1];
         }
-        if (__any_sync(0xffffffffu, raise)) {
+      }
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            float fix[2];
+      for (int r = 0; r < NR; ++r) {
+        float p[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float x = fmaxf(s[r][j], s[r][j + 2]);
+        for (int j = 0; j < 4; ++j) p[j] = ex2(s[r][j] - m[r][j & 1]);
+        l[r][0] += p[0] + p[2];
+        l[r][1] += p[1] + p[3];
+        pb[r][0] = transpose8x8(pack_f16(p[0], p[1]));
+        pb[r][1] = transpose8x8(pack_f16(p[2], p[3]));
+      }
+      // O^T += V^T P^T
+      uint32_t vs[4] = {cur.vs[0], cur.vs[1], cur.vs[2], cur.vs[3]};
+      if (t0 + 16 > sq.ctx) {  // keys past the end: whatever the page holds there counts as 0
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-              x = fmaxf(x, m[r][j]);
-              fix[j] = ex2(m[r][j] - x);
-              m[r][j] = x;
-              l[r][j] *= fix[j];
-            }
+        for (int i = 0; i < 4; ++i)
+          if (t0 + 2 * c + (i & 1) + 8 * (i >> 1) >= sq.ctx) vs[i] = 0;
+      }
+      const uint32_t va = __byte_perm(vs[0], vs[1], 0x5140), vb = __byte_perm(vs[2], vs[3], 0x5140);
 #pragma unroll
-            for (int i = 0; i < KSTEPS; ++i)
+      for (int w = 0; w < Tile<D>::VW; ++w) {
+        const uint32_t sa = e4m3x2_to_f16x2(w < 2 ? va & 0xFFFFu : va >> 16),
+                       sb = e4m3x2_to_f16x2(w < 2 ? vb & 0xFFFFu : vb >> 16);
+        const uint32_t x0 = cur.v[0][w], x1 = cur.v[1][w], x2 = cur.v[2][w], x3 = cur.v[3][w];
+        constexpr uint32_t lo = 0x0F0F0F0Fu;
+        uint32_t fe[4], fo[4], he[4], ho[4];
+        e2m1x8_to_f16x2x4((x0 & lo) | ((x1 << 4) & ~lo), fe);
+        e2m1x8_to_f16x2x4(((x0 >> 4) & lo) | (x1 & ~lo), fo);
+        e2m1x8_to_f16x2x4((x2 & lo) | ((x3 << 4) & ~lo), he);
+        e2m1x8_to_f16x2x4(((x2 >> 4) & lo) | (x3 & ~lo), ho);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[r][i][j] *= fix[j & 1];
-          }
-        }
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t fa[4] = {hmul2(fe[i], sa), hmul2(fo[i], sa), hmul2(he[i], sb), hmul2(ho[i], sb)};
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          float p[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = ex2(s[r][j] - m[r][j & 1]);
-          l[r][0] += p[0] + p[2];
-          l[r][1] += p[1] + p[3];
-          pb[r][0] = transpose8x8(pack_f16(p[0], p[1]));
-          pb[r][1] = transpose8x8(pack_f16(p[2], p[3]));
-        }
-        // O^T += V^T P^T
-        uint32_t vs[4] = {cur.vs[0], cur.vs[1], cur.vs[2], cur.vs[3]};
-        if (t0 + 16 > sq.ctx) {  // keys past the end: whatever the page holds there counts as 0
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (t0 + 2 * c + (i & 1) + 8 * (i >> 1) >= sq.ctx) vs[i] = 0;
-        }
-        const uint32_t va = __byte_perm(vs[0], vs[1], 0x5140), vb = __byte_perm(vs[2], vs[3], 0x5140);
-#pragma unroll
-        for (int w = 0; w < Tile<D>::VW; ++w) {
-          const uint32_t sa = e4m3x2_to_f16x2(w < 2 ? va & 0xFFFFu : va >> 16),
-                         sb = e4m3x2_to_f16x2(w < 2 ? vb & 0xFFFFu : vb >> 16);
-          const uint32_t x0 = cur.v[0][w], x1 = cur.v[1][w], x2 = cur.v[2][w], x3 = cur.v[3][w];
-          constexpr uint32_t lo = 0x0F0F0F0Fu;
-          uint32_t fe[4], fo[4], he[4], ho[4];
-          e2m1x8_to_f16x2x4((x0 & lo) | ((x1 << 4) & ~lo), fe);
-          e2m1x8_to_f16x2x4(((x0 >> 4) & lo) | (x1 & ~lo), fo);
-          e2m1x8_to_f16x2x4((x2 & lo) | ((x3 << 4) & ~lo), he);
-          e2m1x8_to_f16x2x4(((x2 >> 4) & lo) | (x3 & ~lo), ho);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t fa[4] = {hmul2(fe[i], sa), hmul2(fo[i], sa), hmul2(he[i], sb), hmul2(ho[i], sb)};
-#pragma unroll
-            for (int r = 0; r < NR; ++r) mma_f16(o[r][4 * w + i], fa, pb[r][0], pb[r][1]);
-          }
+          for (int r = 0; r < NR; ++r) mma_f16(o[r][4 * w + i], fa, pb[r][0], pb[r][1]);
         }
       }
       cur = nxt;
-      page = page_n;
       page_n = page_nn;
     }
 

@@ -1,0 +1,720 @@
+// Attention of many query rows per key head over the paged NVFP4 cache (prompts and chunks of
+// prompts): out = softmax(scale q K^T) V, both products on the tcgen05 tensor cores.
+//
+// A block takes tiles of 128 query rows of one key head (row = token * G + head of the group, so
+// the G heads that share keys share the expanded keys too) and walks over the keys KT at a time:
+//   producer warps: 4-bit codes and scales from global memory into registers one tile ahead,
+//     expanded to float16 (exact: 2 + 4 significant bits) into shared memory in the 128-byte
+//     swizzle. K rows are the K-major B operand of S = Q K^T; V rows, stored the same way, are
+//     the MN-major B operand of O += P V, so neither is transposed.
+//   MMA warp: S = Q K^T with Q (float16, scaled by a power of two per row) as the A operand in
+//     TMEM, O += P V with P in TMEM. With both A operands in TMEM a product reads shared memory
+//     at half the rate that two shared operands would, which leaves room for the writes of the
+//     expanded tiles (a D = 256 tile is written once per 128 rows).
+//   softmax warps: two threads a row, each half of the keys. S is copied to registers first,
+//     so one S buffer is enough: the next Q K^T runs while the softmax does. O is rescaled only
+//     when a row's maximum rises by more than 2^8 over the one in use (all rows of the tile
+//     then); the weights are below 2^8 in float16, the sums in float32.
+// The order of the tensor pipe is QK(j), PV(j-1), QK(j+1), ...: a softmax has one PV and one QK
+// of time. TMEM: O [0, D), Q [D, 1.5 D), S KT columns, P twice KT / 2.
+//
+// Tiles have different numbers of keys (causal, ragged), so the work (key tiles, plus a few for
+// each row tile's start and end) is dealt to the blocks in equal contiguous runs; a plan kernel
+// writes the prefix sums, and row tiles that lie in more than one block are joined afterwards.
+#include <cuda_bf16.h>
+
+#include "kv_attn.cuh"
+#include "sm100.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kSoftWarps = 8, kProdWarps = 4;
+constexpr int kTcThreads = 32 * (kSoftWarps + kProdWarps + 1);
+constexpr int kPlanThreads = 1024;
+constexpr int kStartCost = 3;  // a row tile's start and end, in key tiles
+
+__host__ __device__ constexpr int key_tile(int D) { return D == 256 ? 64 : 128; }
+__host__ __device__ constexpr int tc_stages(int) { return 3; }
+constexpr int tc_smem(int D) { return 2 * tc_stages(D) * key_tile(D) * D * 2 + 1024; }
+
+// Row tiles of one key head, in order; a tile's share of the work starts at `start`.
+struct RowTile {
+  int b, tile, n_units, pad;
+  long long start;
+  long long pad2;
+};
+
+// keys that the tile's last row sees
+MOE_DEV int tile_keys(const KvAttnArgs& a, const SeqSpan& s, int tile) {
+  if (!a.causal) return s.ctx;
+  const int last = min(s.n_q * a.G, (tile + 1) * kRows) - 1;
+  return min(s.ctx, max(s.ctx - s.n_q + last / a.G + 1, 0));
+}
+
+MOE_DEV int seq_tiles(const KvAttnArgs& a, const SeqSpan& s) {
+  const int rows = s.n_q * a.G;
+  return rows > a.dec_max_rows ? (rows + kRows - 1) / kRows : 0;
+}
+
+// Exclusive block scan of one value per thread (kPlanThreads threads); *total the sum.
+MOE_DEV long long plan_scan(long long v, long long* tmp, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = tmp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    tmp[lane] = w;
+  }
+  __syncthreads();
+  *total = tmp[31];
+  return (warp ? tmp[warp - 1] : 0) + x - v;
+}
+
+// One block: the list of row tiles and the prefix sums of their work.
+__global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttnArgs a, int kt) {
+  MOE_PDL_PROLOGUE();
+  __shared__ long long tmp[32];
+  RowTile* tiles = reinterpret_cast<RowTile*>(a.tiles);
+  // 1. the tiles of every sequence, in order
+  long long at = 0;
+  for (int b0 = 0; b0 < a.n_seqs; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    const int n = b < a.n_seqs ? seq_tiles(a, load_seq(a, b)) : 0;
+    long long sum;
+    const long long first = at + plan_scan(n, tmp, &sum);
+    for (int i = 0; i < n && first + i < a.max_tiles; ++i) {
+      tiles[first + i].b = b;
+      tiles[first + i].tile = i;
+    }
+    at += sum;
+  }
+  __syncthreads();  // (and with it the writes above, for this block)
+  // more tiles than T rows can have: cu_q is not ascending
+  if (at > a.max_tiles && threadIdx.x == 0) atomicExch(a.status, kStatusInvalid);
+  const int n_tiles = (int)min(at, (long long)a.max_tiles);
+  // 2. their work
+  at = 0;
+  for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int units = 0;
+    if (i < n_tiles) {
+      const SeqSpan s = load_seq(a, tiles[i].b);
+      units = max(1, (tile_keys(a, s, tiles[i].tile) + kt - 1) / kt);
+    }
+    long long sum;
+    const long long start = at + plan_scan(i < n_tiles ? units + kStartCost : 0, tmp, &sum);
+    if (i < n_tiles) {
+      tiles[i].n_units = units;
+      tiles[i].start = start;
+    }
+    at += sum;
+  }
+  if (threadIdx.x == 0) {
+    a.plan[0] = at;  // work of one key head
+    a.plan[1] = n_tiles;
+  }
+}
+
+// ---------------------------------------------------------------- TMEM helpers
+MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+
+MOE_DEV void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+
+MOE_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] x B[smem], float16 -> float32, K = 16
+MOE_DEV void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, float16 A and B, float32 accumulator; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// MN-major operand in the 128-byte swizzle: rows of 64 elements along N, one per k; 8 rows are
+// 1024 bytes, the next 64 elements along N are `lbo` bytes on.
+MOE_DEV uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// bar.sync over `n` threads with an OR of their predicates
+MOE_DEV bool bar_or(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+MOE_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+MOE_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A run of key tiles of one row tile.
+struct Run {
+  int b, h, tile, u0, u1, n_units;
+  long long end;  // where the row tile's work ends, counted over all heads
+};
+
+// Walks over the block's runs; every role of the block makes the same walk.
+struct Walk {
+  const RowTile* tiles;
+  long long per_head, at, end;
+  int n_tiles, idx, h;
+
+  MOE_DEV bool next(Run* r) {
+    while (at < end) {
+      const RowTile t = tiles[idx];
+      const long long first = (long long)h * per_head + t.start;
+      const long long lo = at - first;
+      const long long total = t.n_units + kStartCost;
+      const long long hi = min(total, end - first);
+      r->b = t.b;
+      r->h = h;
+      r->tile = t.tile;
+      r->n_units = t.n_units;
+      r->u0 = (int)max(0ll, lo - kStartCost);
+      r->u1 = (int)max(0ll, hi - kStartCost);
+      r->end = first + total;
+      at = first + hi;
+      if (hi == total && ++idx == n_tiles) {
+        idx = 0;
+        ++h;
+      }
+      if (r->u1 > r->u0) return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
+  constexpr int KT = key_tile(D), NS = tc_stages(D);
+  constexpr int HK = KT / 2;                 // keys of a softmax thread
+  constexpr uint32_t kTileBytes = KT * D * 2;
+  constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2, kP = kS + KT;
+  static_assert(kP + KT <= 512, "TMEM columns");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* s_k = smem;
+  uint8_t* s_v = smem + NS * kTileBytes;
+  __shared__ uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+  __shared__ uint64_t q_full, s_full, s_empty, p_full[2], pv_done[2], drained;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ float s_x[2][kRows];
+  __shared__ int s_e[2][kRows];
+  __shared__ int s_idx;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&k_full[s], kProdWarps);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], kProdWarps);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(&q_full, kSoftWarps);
+    mbar_init(&s_full, 1);
+    mbar_init(&s_empty, kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(&drained, 1);
+    fence_barrier_init();
+    s_abort = 0;
+  }
+  if (warp == kSoftWarps + kProdWarps) tmem_alloc(&s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  MOE_PDL_PROLOGUE();
+
+  // ---- this block's run of the work
+  Walk walk;
+  walk.tiles = reinterpret_cast<const RowTile*>(a.tiles);
+  walk.per_head = a.plan[0];
+  walk.n_tiles = (int)a.plan[1];
+  const long long total = walk.per_head * a.cache.Hkv;
+  const int grid = (int)min((long long)gridDim.x, total);
+  walk.at = walk.end = 0;
+  if ((int)blockIdx.x < grid) {
+    walk.at = total * blockIdx.x / grid;
+    walk.end = total * (blockIdx.x + 1) / grid;
+    walk.h = (int)(walk.at / walk.per_head);
+    const long long x = walk.at - walk.h * walk.per_head;
+    if (warp == 0) {  // the last tile that starts at or before x: 32 probes a round
+      int lo = 0, hi = walk.n_tiles;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int probe = lo + lane * step;
+        const bool le = probe < hi && walk.tiles[probe].start <= x;
+        const int n = __popc(__ballot_sync(0xffffffffu, le));
+        lo += (n - 1) * step;
+        hi = min(hi, lo + step);
+      }
+      if (lane == 0) s_idx = lo;
+    }
+  }
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  __syncthreads();
+  walk.idx = s_idx;
+
+  if (warp < kSoftWarps) {
+    // ================================================================ softmax
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    uint32_t tc = 0;  // key tiles so far
+    bool ok = true;
+    Run run;
+    while (ok && walk.next(&run)) {
+      const SeqSpan sq = load_seq(a, run.b);
+      const int rows = sq.n_q * a.G, rr = run.tile * kRows + row;
+      const bool live = rr < rows;
+      const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
+      const float ks = a.scale * (a.cache.k_ts ? a.cache.k_ts[run.h] : 1.0f) * kLog2e;
+      // ---- Q: this thread's half of the row
+      float fac;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride +
+                                                          (int64_t)head * D + half * (D / 2));
+        uint4 raw[D / 16];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
+          mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
+          mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
+          mx = __vmaxu2(mx, raw[i].w & 0x7FFF7FFFu);
+        }
+        s_e[half][row] = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;
+        named_bar_sync(1, kSoftWarps * 32);
+        const int e = max(max(s_e[0][row], s_e[1][row]), -100);
+        // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
+        const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
+        fac = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          uint32_t f[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w[4] = {raw[4 * i + j].x, raw[4 * i + j].y, raw[4 * i + j].z, raw[4 * i + j].w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              f[4 * j + u] = pack_f16(bf16_to_f32(w[u] & 0xFFFFu) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
+          }
+          tmem_st16(tl + kQ + half * (D / 4) + 16 * i, f);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
+      // keys that every row of the tile sees
+      const int first_tok = run.tile * kRows / a.G;
+      const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
+      float m = kNoMax;
+      uint64_t l2 = pack2(0.0f, 0.0f);
+      const uint64_t fac2 = pack2(fac, fac);
+      for (int u = run.u0; u < run.u1; ++u, ++tc) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full, tc & 1, &s_abort, a.status));
+        tc_fence_after();
+        uint32_t s[HK];
+#pragma unroll
+        for (int i = 0; i < HK / 32; ++i)
+          tmem_ld32(tl + kS + half * HK + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * i]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty);
+        const int k0 = u * KT + half * HK;
+        if (u * KT + KT > lim_min) {
+#pragma unroll
+          for (int i = 0; i < HK; ++i)
+            if (k0 + i >= lim) s[i] = 0xff800000u;
+        }
+        float mx = __uint_as_float(s[0]);
+#pragma unroll
+        for (int i = 1; i < HK; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+        mx *= fac;
+        const bool first = u == run.u0;
+        if (bar_or(1, kSoftWarps * 32, mx > m + kRaise || !ok)) {
+          s_x[half][row] = mx;
+          if (bar_or(2, kSoftWarps * 32, !ok)) {
+            ok = false;
+            break;
+          }
+          const float top = fmaxf(fmaxf(s_x[0][row], s_x[1][row]), m);
+          if (!first) {
+            const float fix = ex2(m - top);
+            float a0, a1;
+            unpack2(l2, a0, a1);
+            l2 = pack2(a0 * fix, a1 * fix);
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_abort, a.status));
+            tc_fence_after();
+            if (ok) {
+#pragma unroll
+              for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tl + kO + half * (D / 2) + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+                tmem_st32(tl + kO + half * (D / 2) + c, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          m = top;
+          bar_or(1, kSoftWarps * 32, false);  // s_x is free again
+        }
+        const uint64_t nm2 = pack2(-m, -m);
+        uint32_t p[HK / 2];
+#pragma unroll
+        for (int i = 0; i < HK / 2; ++i) {
+          const uint64_t x = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), fac2, nm2);
+          float x0, x1;
+          unpack2(x, x0, x1);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          l2 = add2(l2, pack2(x0, x1));
+          p[i] = pack_f16(x0, x1);
+        }
+        if (tc >= 2)  // the product that read this P buffer two tiles ago
+          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[tc & 1], ((tc >> 1) - 1) & 1, &s_abort, a.status)) && ok;
+        const uint32_t tp = tl + kP + (tc & 1) * (KT / 2) + half * (HK / 2);
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < HK / 32; ++i) tmem_st16(tp + 16 * i, &p[16 * i]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[tc & 1]);
+      }
+      // ---- the run's result
+      float l0, l1;
+      unpack2(l2, l0, l1);
+      s_x[half][row] = l0 + l1;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_abort, a.status));
+      tc_fence_after();
+      if (bar_or(1, kSoftWarps * 32, !ok)) break;
+      const float ll = s_x[0][row] + s_x[1][row];
+      const bool whole = run.u0 == 0 && run.u1 == run.n_units;
+      const float vts = a.cache.v_ts ? a.cache.v_ts[run.h] : 1.0f;
+      const float f = !whole ? 1.0f : ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
+      const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
+      const int side = run.u0 > 0 ? 0 : 1;
+      float* part = a.partial + ((size_t)blockIdx.x * 2 + side) * a.part_stride;
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tl + kO + half * (D / 2) + c, o);
+        tmem_ld_wait();
+        if (whole) {
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + half * (D / 2) + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * j]) * f,
+                                                               __uint_as_float(o[8 * i + 2 * j + 1]) * f);
+                w[j] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(part + 2 * kRows + row * D + half * (D / 2) + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                 __uint_as_float(o[4 * i + 3]));
+        }
+      }
+      if (half == 0) {
+        if (!whole) {
+          part[row] = m;
+          part[kRows + row] = ll;
+        } else if (live && a.lse) {
+          a.lse[out_row] = ll == 0.0f ? -INFINITY : (m + log2f(ll)) * kLn2;
+        }
+      }
+      if (!whole && side == 1 && threadIdx.x == 0) {
+        int last = blockIdx.x + 1;
+        while (total * (last + 1) / grid < run.end) ++last;
+        a.meta[blockIdx.x] = make_int4(run.b, run.h, run.tile * kRows, last);
+      }
+      tc_fence_before();
+      named_bar_sync(1, kSoftWarps * 32);  // s_x and s_e are free again, O has been read
+    }
+  } else if (warp < kSoftWarps + kProdWarps) {
+    // ================================================================ producers
+    // 32 elements at a time: 8 rows x 4 parts of 16 bytes a warp, so that the loads are whole
+    // rows and the 16-byte stores of 8 lanes fall into 8 different places of the swizzle
+    constexpr int P = D / 32;                    // parts of a row
+    constexpr int STEPS = KT / 8 * P / 16;       // octets of rows x parts, 16 of them a turn
+    const int pw = warp - kSoftWarps;
+    uint32_t tc = 0;
+    bool ok = true;
+    Run run;
+    struct Piece {
+      uint4 codes[STEPS];
+      uint32_t scales[STEPS];
+    };
+    auto load = [&](Piece& x, const uint8_t* codes, const uint8_t* scales, int u, int h, int ctx, const int32_t* table) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int octet = (i * kProdWarps + pw) * 4 + (lane >> 3);
+        const int part = octet % P, t = u * KT + octet / P * 8 + (lane & 7);
+        x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+        x.scales[i] = 0u;
+        if (t < ctx) {
+          const int page = __ldg(table + (t >> a.page_shift));
+          if (page >= 0 && page < a.cache.n_pages) {
+            const int64_t r = ((int64_t)page * a.cache.Hkv + h) * a.cache.page_size + (t & (a.cache.page_size - 1));
+            x.codes[i] = __ldg(reinterpret_cast<const uint4*>(codes + r * (D / 2)) + part);
+            x.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + r * (D / 16)) + part);
+          } else {
+            atomicExch(a.status, kStatusInvalid);  // its rows count as zeros
+          }
+        }
+      }
+    };
+    auto store = [&](const Piece& x, uint8_t* tile) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int octet = (i * kProdWarps + pw) * 4 + (lane >> 3);
+        const int part = octet % P, row = octet / P * 8 + (lane & 7);
+        uint8_t* dst = tile + (part >> 1) * (KT * 128) + row * 128;
+        const int chunk = (part & 1) * 4;
+        const uint32_t w[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
+        const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(x.scales[i], 0, 0x0000)),
+                       s1 = e4m3x2_to_f16x2(__byte_perm(x.scales[i], 0, 0x0011));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t f[4];
+          e2m1x8_to_f16x2x4(w[j], f);
+          const uint32_t s = j < 2 ? s0 : s1;
+          *reinterpret_cast<uint4*>(dst + (((chunk + j) ^ (row & 7)) << 4)) =
+              make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
+        }
+      }
+    };
+    while (ok && walk.next(&run)) {
+      const SeqSpan sq = load_seq(a, run.b);
+      const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
+      Piece xk, xv;
+      load(xk, a.cache.k_codes, a.cache.k_scales, run.u0, run.h, sq.ctx, table);
+      for (int u = run.u0; u < run.u1; ++u, ++tc) {
+        const uint32_t s = tc % NS, ph = (tc / NS) & 1;
+        load(xv, a.cache.v_codes, a.cache.v_scales, u, run.h, sq.ctx, table);
+        ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[s], ph ^ 1, &s_abort, a.status));
+        if (!ok) break;
+        store(xk, s_k + s * kTileBytes);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[s]);
+        if (u + 1 < run.u1) load(xk, a.cache.k_codes, a.cache.k_scales, u + 1, run.h, sq.ctx, table);
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], ph ^ 1, &s_abort, a.status));
+        if (!ok) break;
+        store(xv, s_v + s * kTileBytes);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[s]);
+      }
+    }
+  } else {
+    // ================================================================ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_f16(kRows, KT, false), idesc_pv = idesc_f16(kRows, D, true);
+      uint32_t tc = 0, items = 0;
+      bool ok = true;
+      Run run;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = mbar_wait(bar, parity, &s_abort, a.status);
+      };
+      while (ok && walk.next(&run)) {
+        wait(&q_full, items & 1);
+        ++items;
+        const int n = run.u1 - run.u0;
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) {  // S = Q K^T of tile j
+            const uint32_t t = tc + j, s = t % NS;
+            wait(&k_full[s], (t / NS) & 1);
+            wait(&s_empty, (t & 1) ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t base = smem_u32(s_k + s * kTileBytes);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_f16_ts(tmem + kS, tmem + kQ + 8 * kk, sdesc_sw128(base + (kk / 4) * (KT * 128) + (kk % 4) * 32),
+                         idesc_qk, kk ? 1u : 0u);
+            mma_commit(&s_full);
+            mma_commit(&k_empty[s]);
+          }
+          if (j > 0) {  // O += P V of tile j - 1
+            const uint32_t t = tc + j - 1, s = t % NS;
+            wait(&v_full[s], (t / NS) & 1);
+            wait(&p_full[t & 1], (t >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t base = smem_u32(s_v + s * kTileBytes);
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              mma_f16_ts(tmem + kO, tmem + kP + (t & 1) * (KT / 2) + 8 * kk, sdesc_mn_sw128(base + kk * 2048, KT * 128),
+                         idesc_pv, (j > 1 || kk) ? 1u : 0u);
+            mma_commit(&pv_done[t & 1]);
+            mma_commit(&v_empty[s]);
+          }
+        }
+        tc += n;
+      }
+      // TMEM and shared memory are given back only after every product is done with them
+      mma_commit(&drained);
+      volatile int no_abort = 0;
+      mbar_wait(&drained, 0, &no_abort, a.status);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + kProdWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the row tiles that lie in several blocks: one block per (run that ends inside a row
+// tile, 8 rows), a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) kv_attn_tc_join_kernel(const KvAttnArgs a) {
+  MOE_PDL_PROLOGUE();
+  const int4 meta = a.meta[blockIdx.x];
+  if (meta.x < 0) return;
+  const SeqSpan sq = load_seq(a, meta.x);
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, rr = meta.z + row;
+  if (rr >= sq.n_q * a.G) return;
+  const int first = blockIdx.x, last = meta.w;
+  auto part = [&](int i) { return a.partial + ((size_t)i * 2 + (i == first ? 1 : 0)) * a.part_stride; };
+  constexpr int V = D / 64;  // float2 of a lane
+  float mm = kNoMax, ll = 0.0f;
+  float2 acc[V] = {};
+  for (int i = first; i <= last; ++i) {
+    const float* p = part(i);
+    const float pm = p[row], top = fmaxf(mm, pm);
+    const float f0 = ex2(mm - top), f1 = ex2(pm - top);
+    mm = top;
+    ll = ll * f0 + p[kRows + row] * f1;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float2 v = reinterpret_cast<const float2*>(p + 2 * kRows + row * D)[j * 32 + lane];
+      acc[j].x = acc[j].x * f0 + v.x * f1;
+      acc[j].y = acc[j].y * f0 + v.y * f1;
+    }
+  }
+  const int tok = rr / a.G, head = meta.y * a.G + rr - tok * a.G;
+  const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
+  const float vts = a.cache.v_ts ? a.cache.v_ts[meta.y] : 1.0f;
+  const float f = ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    reinterpret_cast<__nv_bfloat162*>(a.out + out_row * D)[j * 32 + lane] = __floats2bfloat162_rn(acc[j].x * f, acc[j].y * f);
+  if (a.lse && lane == 0) a.lse[out_row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_tc(const KvAttnArgs& a, int num_sms, cudaStream_t st) {
+  cudaError_t e = launch_pdl(kv_attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, key_tile(D));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv_attn_tc_kernel<D>, dim3(num_sms), dim3(kTcThreads), tc_smem(D), st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv_attn_tc_join_kernel<D>, dim3(num_sms, kRows / 8), dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+size_t kv_attn_tc_part_floats(int D) { return (size_t)kRows * (D + 2); }
+int kv_attn_tc_max_tiles(int64_t T, int n_seqs, int G) { return (int)(T * G / kRows + n_seqs + 1); }
+size_t kv_attn_tc_tiles_bytes(int64_t T, int n_seqs, int G) {
+  return (size_t)kv_attn_tc_max_tiles(T, n_seqs, G) * sizeof(RowTile);
+}
+
+cudaError_t set_wait_limit_kv_attn_tc(unsigned long long ns) { return set_wait_limit_here(ns); }
+
+cudaError_t init_kv_attn_tc_attributes() {
+  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_tc_kernel<64>, at, tc_smem(64));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_attn_tc_kernel<128>, at, tc_smem(128));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_attn_tc_kernel<256>, at, tc_smem(256));
+  return e;
+}
+
+cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st) {
+  if (D == 64) return launch_tc<64>(a, num_sms, st);
+  if (D == 128) return launch_tc<128>(a, num_sms, st);
+  return launch_tc<256>(a, num_sms, st);
+}
+
+}  // namespace moe
