@@ -3,8 +3,9 @@
 //
 // A block takes tiles of 128 query rows of one key head (row = token * G + head of the group, so
 // the G heads that share keys share the expanded keys too) and walks over the keys KT at a time:
-//   producer warps: 4-bit codes and scales from global memory into registers one tile ahead,
-//     expanded to float16 (exact: 2 + 4 significant bits) into shared memory in the 128-byte
+//   loader warp: a tile's codes and scales by bulk copies (a page's rows of one head are
+//     contiguous) into a ring of raw tiles, several ahead.
+//   expander warps: raw tiles to float16 (exact: 2 + 4 significant bits) in the 128-byte
 //     swizzle. K rows are the K-major B operand of S = Q K^T; V rows, stored the same way, are
 //     the MN-major B operand of O += P V, so neither is transposed.
 //   MMA warp: S = Q K^T with Q (float16, scaled by a power of two per row) as the A operand in
@@ -31,14 +32,17 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kSoftWarps = 8, kProdWarps = 4;
-constexpr int kTcThreads = 32 * (kSoftWarps + kProdWarps + 1);
+constexpr int kSoftWarps = 8, kExpWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kExpWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kTcThreads = 32 * (kSoftWarps + kExpWarps + 4);  // four whole warpgroups
 constexpr int kPlanThreads = 1024;
 constexpr int kStartCost = 3;  // a row tile's start and end, in key tiles
 
 __host__ __device__ constexpr int key_tile(int D) { return D == 256 ? 64 : 128; }
-__host__ __device__ constexpr int tc_stages(int) { return 3; }
-constexpr int tc_smem(int D) { return 2 * tc_stages(D) * key_tile(D) * D * 2 + 1024; }
+constexpr int kTcStages = 2;   // expanded tiles of K, and of V
+constexpr int kRawSlots = 8;   // raw tiles, K and V in turn
+__host__ __device__ constexpr int raw_bytes(int D) { return key_tile(D) * (D / 2 + D / 16); }
+constexpr int tc_smem(int D) { return 2 * kTcStages * key_tile(D) * D * 2 + kRawSlots * raw_bytes(D) + 1024; }
 
 // Row tiles of one key head, in order; a tile's share of the work starts at `start`.
 struct RowTile {
@@ -175,6 +179,24 @@ MOE_DEV uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The block is launched with 128 registers a thread (65536): the 256 softmax threads take 168,
+// the 128 expander threads 96 and the last warpgroup 80, which adds up to the same.
+template <int N>
+MOE_DEV void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+MOE_DEV void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// true in one lane of the (whole) warp, the same one every time
+MOE_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // bar.sync over `n` threads with an OR of their predicates
 MOE_DEV bool bar_or(int id, int n, bool p) {
   uint32_t r;
@@ -204,6 +226,27 @@ MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// mbar_wait with the limit read once per block: short in code (the roles of a block share the
+// instruction caches) and without a load from global memory in every wait.
+struct Patience {
+  volatile int abort;
+  unsigned long long limit;
+};
+MOE_DEV bool wait_soon(uint64_t* bar, uint32_t parity, Patience* w, int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (w->abort) return false;
+    if (globaltimer_ns() - t0 > w->limit) {
+      w->abort = 1;
+      atomicExch(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 
 // A run of key tiles of one row tile.
@@ -245,7 +288,7 @@ struct Walk {
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
-  constexpr int KT = key_tile(D), NS = tc_stages(D);
+  constexpr int KT = key_tile(D), NS = kTcStages;
   constexpr int HK = KT / 2;                 // keys of a softmax thread
   constexpr uint32_t kTileBytes = KT * D * 2;
   constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2, kP = kS + KT;
@@ -254,20 +297,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* s_k = smem;
   uint8_t* s_v = smem + NS * kTileBytes;
+  uint8_t* s_raw = smem + 2 * NS * kTileBytes;
+  __shared__ uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+  __shared__ uint32_t s_bad[kRawSlots];  // groups of 16 keys whose page number is outside the cache
   __shared__ uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
   __shared__ uint64_t q_full, s_full, s_empty, p_full[2], pv_done[2], drained;
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
+  __shared__ Patience s_wait;
   __shared__ float s_x[2][kRows];
   __shared__ int s_e[2][kRows];
   __shared__ int s_idx;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&k_full[s], kProdWarps);
+      mbar_init(&k_full[s], kExpWarps);
       mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], kProdWarps);
+      mbar_init(&v_full[s], kExpWarps);
       mbar_init(&v_empty[s], 1);
+    }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kExpWarps);
     }
     mbar_init(&q_full, kSoftWarps);
     mbar_init(&s_full, 1);
@@ -278,9 +328,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
     }
     mbar_init(&drained, 1);
     fence_barrier_init();
-    s_abort = 0;
+    s_wait.abort = 0;
+    s_wait.limit = wait_limit_ns();
   }
-  if (warp == kSoftWarps + kProdWarps) tmem_alloc(&s_tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -319,6 +370,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
+    more_registers<168>();
     const int half = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -377,7 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       uint64_t l2 = pack2(0.0f, 0.0f);
       const uint64_t fac2 = pack2(fac, fac);
       for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full, tc & 1, &s_abort, a.status));
+        ok = __all_sync(0xffffffffu, wait_soon(&s_full, tc & 1, &s_wait, a.status));
         tc_fence_after();
         uint32_t s[HK];
 #pragma unroll
@@ -410,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
             float a0, a1;
             unpack2(l2, a0, a1);
             l2 = pack2(a0 * fix, a1 * fix);
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_abort, a.status));
+            ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
             tc_fence_after();
             if (ok) {
 #pragma unroll
@@ -441,7 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
           p[i] = pack_f16(x0, x1);
         }
         if (tc >= 2)  // the product that read this P buffer two tiles ago
-          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[tc & 1], ((tc >> 1) - 1) & 1, &s_abort, a.status)) && ok;
+          ok = __all_sync(0xffffffffu, wait_soon(&pv_done[tc & 1], ((tc >> 1) - 1) & 1, &s_wait, a.status)) && ok;
         const uint32_t tp = tl + kP + (tc & 1) * (KT / 2) + half * (HK / 2);
         tc_fence_after();
 #pragma unroll
@@ -455,7 +507,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       float l0, l1;
       unpack2(l2, l0, l1);
       s_x[half][row] = l0 + l1;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_abort, a.status));
+      if (ok) ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
       tc_fence_after();
       if (bar_or(1, kSoftWarps * 32, !ok)) break;
       const float ll = s_x[0][row] + s_x[1][row];
@@ -509,92 +561,149 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       tc_fence_before();
       named_bar_sync(1, kSoftWarps * 32);  // s_x and s_e are free again, O has been read
     }
-  } else if (warp < kSoftWarps + kProdWarps) {
-    // ================================================================ producers
-    // 32 elements at a time: 8 rows x 4 parts of 16 bytes a warp, so that the loads are whole
-    // rows and the 16-byte stores of 8 lanes fall into 8 different places of the swizzle
-    constexpr int P = D / 32;                    // parts of a row
-    constexpr int STEPS = KT / 8 * P / 16;       // octets of rows x parts, 16 of them a turn
+  } else if (warp < kMmaWarp) {
+    // ================================================================ expanders
+    // 32 elements (16 bytes of codes) a lane and step, lanes side by side in the raw tile. The
+    // four 16-byte stores of a lane go out in an order that depends on its place in the row, so
+    // that 8 lanes always fall into 8 different places of the swizzle.
+    fewer_registers<96>();
+    constexpr int P = D / 32;                 // lanes of a row
+    constexpr int STEPS = KT * P / (32 * kExpWarps);
     const int pw = warp - kSoftWarps;
-    uint32_t tc = 0;
+    uint32_t n_raw = 0;
     bool ok = true;
     Run run;
-    struct Piece {
-      uint4 codes[STEPS];
-      uint32_t scales[STEPS];
-    };
-    auto load = [&](Piece& x, const uint8_t* codes, const uint8_t* scales, int u, int h, int ctx, const int32_t* table) {
+    while (ok && walk.next(&run)) {
+      const int ctx = load_seq(a, run.b).ctx;
+#pragma unroll 1
+      for (int i = 2 * run.u0; i < 2 * run.u1; ++i, ++n_raw) {  // K and V of each tile in turn
+        const bool is_v = i & 1;
+        const uint32_t slot = n_raw % kRawSlots, s = (n_raw >> 1) % NS;
+        ok = __all_sync(0xffffffffu, wait_soon(&raw_full[slot], (n_raw / kRawSlots) & 1, &s_wait, a.status)) &&
+             __all_sync(0xffffffffu, wait_soon(is_v ? &v_empty[s] : &k_empty[s], ((n_raw / (2 * NS)) & 1) ^ 1, &s_wait,
+                                               a.status));
+        if (!ok) break;
+        const uint8_t* raw = s_raw + slot * raw_bytes(D);
+        uint8_t* tile = (is_v ? s_v : s_k) + s * kTileBytes;
+        const uint32_t bad = s_bad[slot];
+        const int left = ctx - (i >> 1) * KT;
+        uint4 codes[STEPS];
+        uint32_t scales[STEPS];
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int octet = (i * kProdWarps + pw) * 4 + (lane >> 3);
-        const int part = octet % P, t = u * KT + octet / P * 8 + (lane & 7);
-        x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-        x.scales[i] = 0u;
-        if (t < ctx) {
-          const int page = __ldg(table + (t >> a.page_shift));
-          if (page >= 0 && page < a.cache.n_pages) {
-            const int64_t r = ((int64_t)page * a.cache.Hkv + h) * a.cache.page_size + (t & (a.cache.page_size - 1));
-            x.codes[i] = __ldg(reinterpret_cast<const uint4*>(codes + r * (D / 2)) + part);
-            x.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + r * (D / 16)) + part);
-          } else {
-            atomicExch(a.status, kStatusInvalid);  // its rows count as zeros
+        for (int step = 0; step < STEPS; ++step) {
+          const int unit = (step * kExpWarps + pw) * 32 + lane;
+          codes[step] = reinterpret_cast<const uint4*>(raw)[unit];
+          scales[step] = reinterpret_cast<const uint16_t*>(raw + KT * (D / 2))[unit];
+        }
+#pragma unroll
+        for (int step = 0; step < STEPS; ++step) {
+          const int unit = (step * kExpWarps + pw) * 32 + lane, row = unit / P, part = unit % P;
+          // keys past the end, and pages outside the cache, count as zeros
+          const uint32_t sc2 = row >= left || ((bad >> (row / 16)) & 1u) ? 0u : scales[step];
+          uint8_t* dst = tile + (part >> 1) * (KT * 128) + row * 128;
+          uint32_t w0 = codes[step].x, w1 = codes[step].y, w2 = codes[step].z, w3 = codes[step].w;
+          uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(sc2, 0, 0x0000)), s1 = e4m3x2_to_f16x2(__byte_perm(sc2, 0, 0x0011));
+          // turn: 2 bits for the 4 pairs of lanes of a row of 8, 1 (as 0 or 2) for 2 pairs of 4
+          const int turn = D == 256 ? part >> 1 : D == 128 ? part & 2 : 0;
+          if (turn & 2) {
+            uint32_t x = w0; w0 = w2; w2 = x;
+            x = w1; w1 = w3; w3 = x;
+            x = s0; s0 = s1; s1 = x;
+          }
+          if (turn & 1) {
+            uint32_t x = w0; w0 = w1; w1 = x;
+            x = w2; w2 = w3; w3 = x;
+          }
+          const uint32_t w[4] = {w0, w1, w2, w3};
+          const int chunk = ((part & 1) * 4 + turn) ^ (row & 7);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t f[4];
+            e2m1x8_to_f16x2x4(w[j], f);
+            const uint32_t sc = j < 2 ? s0 : s1;
+            *reinterpret_cast<uint4*>(dst + ((chunk ^ j) << 4)) =
+                make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
           }
         }
-      }
-    };
-    auto store = [&](const Piece& x, uint8_t* tile) {
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int octet = (i * kProdWarps + pw) * 4 + (lane >> 3);
-        const int part = octet % P, row = octet / P * 8 + (lane & 7);
-        uint8_t* dst = tile + (part >> 1) * (KT * 128) + row * 128;
-        const int chunk = (part & 1) * 4;
-        const uint32_t w[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
-        const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(x.scales[i], 0, 0x0000)),
-                       s1 = e4m3x2_to_f16x2(__byte_perm(x.scales[i], 0, 0x0011));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t f[4];
-          e2m1x8_to_f16x2x4(w[j], f);
-          const uint32_t s = j < 2 ? s0 : s1;
-          *reinterpret_cast<uint4*>(dst + (((chunk + j) ^ (row & 7)) << 4)) =
-              make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[slot]);
+          mbar_arrive(is_v ? &v_full[s] : &k_full[s]);
         }
-      }
-    };
-    while (ok && walk.next(&run)) {
-      const SeqSpan sq = load_seq(a, run.b);
-      const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
-      Piece xk, xv;
-      load(xk, a.cache.k_codes, a.cache.k_scales, run.u0, run.h, sq.ctx, table);
-      for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        const uint32_t s = tc % NS, ph = (tc / NS) & 1;
-        load(xv, a.cache.v_codes, a.cache.v_scales, u, run.h, sq.ctx, table);
-        ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[s], ph ^ 1, &s_abort, a.status));
-        if (!ok) break;
-        store(xk, s_k + s * kTileBytes);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[s]);
-        if (u + 1 < run.u1) load(xk, a.cache.k_codes, a.cache.k_scales, u + 1, run.h, sq.ctx, table);
-        ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], ph ^ 1, &s_abort, a.status));
-        if (!ok) break;
-        store(xv, s_v + s * kTileBytes);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[s]);
       }
     }
   } else {
-    // ================================================================ MMA
-    if (lane == 0) {
+    fewer_registers<80>();
+    if (warp == kLoadWarp) {
+      // ================================================================ loader
+      // a lane copies one page's part of the tile: at most KT / 16 pages
+      uint32_t n_raw = 0;
+      bool ok = true;
+      Run run;
+      const int ps = a.cache.page_size;
+      const int rows = min(ps, KT);               // of a copy
+      const int copies = KT / rows;
+      while (ok && walk.next(&run)) {
+        const int ctx = load_seq(a, run.b).ctx;
+        const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
+        auto page_of = [&](int u) {
+          const int t = u * KT + lane * rows;
+          return lane < copies && t < ctx ? __ldg(table + (t >> a.page_shift)) : 0;
+        };
+        int page = page_of(run.u0);
+        for (int u = run.u0; u < run.u1 && ok; ++u) {
+          const int next = page_of(u + 1);
+          const int t = u * KT + lane * rows;
+          const bool wanted = lane < copies && t < ctx;
+          const bool good = wanted && page >= 0 && page < a.cache.n_pages;
+          if (wanted && !good) atomicExch(a.status, kStatusInvalid);
+          // a copy of `rows` keys is rows / 16 groups of 16
+          uint32_t bad = 0;
+          const uint32_t lanes = __ballot_sync(0xffffffffu, wanted && !good);
+          for (int i = 0; i < copies; ++i)
+            if ((lanes >> i) & 1u) bad |= ((1u << (rows / 16)) - 1u) << (i * (rows / 16));
+          const uint32_t n_good = __popc(__ballot_sync(0xffffffffu, good));
+          const int64_t row = ((int64_t)page * a.cache.Hkv + run.h) * ps + (t & (ps - 1));
+#pragma unroll
+          for (int kv = 0; kv < 2 && ok; ++kv, ++n_raw) {
+            const uint32_t slot = n_raw % kRawSlots;
+            ok = __all_sync(0xffffffffu, wait_soon(&raw_empty[slot], ((n_raw / kRawSlots) & 1) ^ 1, &s_wait, a.status));
+            if (!ok) break;
+            uint8_t* raw = s_raw + slot * raw_bytes(D);
+            if (lane == 0) {
+              s_bad[slot] = bad;
+              mbar_arrive_expect_tx(&raw_full[slot], n_good * rows * (D / 2 + D / 16));
+            }
+            __syncwarp();
+            if (good) {
+              bulk_g2s(raw + lane * rows * (D / 2), (kv ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2),
+                       rows * (D / 2), &raw_full[slot]);
+              bulk_g2s(raw + KT * (D / 2) + lane * rows * (D / 16),
+                       (kv ? a.cache.v_scales : a.cache.k_scales) + row * (D / 16), rows * (D / 16), &raw_full[slot]);
+            }
+          }
+          page = next;
+        }
+      }
+      // no copy may still be landing when the block ends
+      __syncwarp();
+      for (uint32_t j = n_raw > kRawSlots ? n_raw - kRawSlots : 0; j < n_raw; ++j) {
+        volatile int no_abort = 0;
+        mbar_wait(&raw_full[j % kRawSlots], (j / kRawSlots) & 1, &no_abort, a.status);
+      }
+    } else if (warp == kMmaWarp) {
+      // ================================================================ MMA
+      // The whole warp takes the walk and the waits, so that descriptors are the same in every
+      // lane (uniform registers); one elected lane issues.
       constexpr uint32_t idesc_qk = idesc_f16(kRows, KT, false), idesc_pv = idesc_f16(kRows, D, true);
       uint32_t tc = 0, items = 0;
       bool ok = true;
       Run run;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = mbar_wait(bar, parity, &s_abort, a.status);
+        ok = ok && __all_sync(0xffffffffu, wait_soon(bar, parity, &s_wait, a.status));
       };
+      const uint64_t desc_k = sdesc_sw128(smem_u32(s_k)), desc_v = sdesc_mn_sw128(smem_u32(s_v), KT * 128);
       while (ok && walk.next(&run)) {
         wait(&q_full, items & 1);
         ++items;
@@ -606,13 +715,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
             wait(&s_empty, (t & 1) ^ 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t base = smem_u32(s_k + s * kTileBytes);
+            const uint64_t desc = desc_k + s * (kTileBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_f16_ts(tmem + kS, tmem + kQ + 8 * kk, sdesc_sw128(base + (kk / 4) * (KT * 128) + (kk % 4) * 32),
-                         idesc_qk, kk ? 1u : 0u);
-            mma_commit(&s_full);
-            mma_commit(&k_empty[s]);
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_f16_ts(tmem + kS, tmem + kQ + 8 * kk, desc + (((kk / 4) * (KT * 128) + (kk % 4) * 32) >> 4), idesc_qk,
+                           kk ? 1u : 0u);
+              mma_commit(&s_full);
+              mma_commit(&k_empty[s]);
+            }
+            __syncwarp();
           }
           if (j > 0) {  // O += P V of tile j - 1
             const uint32_t t = tc + j - 1, s = t % NS;
@@ -620,27 +732,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
             wait(&p_full[t & 1], (t >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t base = smem_u32(s_v + s * kTileBytes);
+            const uint64_t desc = desc_v + s * (kTileBytes >> 4);
+            const uint32_t p = tmem + kP + (t & 1) * (KT / 2), add = j > 1 ? 1u : 0u;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              mma_f16_ts(tmem + kO, tmem + kP + (t & 1) * (KT / 2) + 8 * kk, sdesc_mn_sw128(base + kk * 2048, KT * 128),
-                         idesc_pv, (j > 1 || kk) ? 1u : 0u);
-            mma_commit(&pv_done[t & 1]);
-            mma_commit(&v_empty[s]);
+              for (int kk = 0; kk < KT / 16; ++kk)
+                mma_f16_ts(tmem + kO, p + 8 * kk, desc + ((kk * 2048) >> 4), idesc_pv, kk ? 1u : add);
+              mma_commit(&pv_done[t & 1]);
+              mma_commit(&v_empty[s]);
+            }
+            __syncwarp();
           }
         }
         tc += n;
       }
       // TMEM and shared memory are given back only after every product is done with them
-      mma_commit(&drained);
-      volatile int no_abort = 0;
-      mbar_wait(&drained, 0, &no_abort, a.status);
+      if (elect_one()) {
+        mma_commit(&drained);
+        volatile int no_abort = 0;
+        mbar_wait(&drained, 0, &no_abort, a.status);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kProdWarps) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
