@@ -12,12 +12,13 @@
 //     TMEM, O += P V with P in TMEM. With both A operands in TMEM a product reads shared memory
 //     at half the rate that two shared operands would, which leaves room for the writes of the
 //     expanded tiles (a D = 256 tile is written once per 128 rows).
-//   softmax warps: two threads a row, each half of the keys. S is copied to registers first,
-//     so one S buffer is enough: the next Q K^T runs while the softmax does. O is rescaled only
-//     when a row's maximum rises by more than 2^8 over the one in use (all rows of the tile
-//     then); the weights are below 2^8 in float16, the sums in float32.
-// The order of the tensor pipe is QK(j), PV(j-1), QK(j+1), ...: a softmax has one PV and one QK
-// of time. TMEM: O [0, D), Q [D, 1.5 D), S KT columns, P twice KT / 2.
+//   softmax warps: two groups of 128 threads, a thread a row, that take the key tiles in turn,
+//     so that one group's exponentials (the busiest unit, 16 a cycle) run beside the other's
+//     maxima and copies. P overwrites S in TMEM. The maximum in use passes from tile to tile
+//     through shared memory; O is rescaled only when a row's maximum rises by more than 2^8 over
+//     it; the weights are below 2^8 in float16, the sums in float32.
+// The order of the tensor pipe is QK(j), PV(j-1), QK(j+1), ... TMEM: O [0, D), Q [D, 1.5 D), two
+// S / P buffers of KT columns.
 //
 // Tiles have different numbers of keys (causal, ragged), so the work (key tiles, plus a few for
 // each row tile's start and end) is dealt to the blocks in equal contiguous runs; a plan kernel
@@ -32,11 +33,17 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kSoftWarps = 8, kExpWarps = 4;
+constexpr int kSoftWarps = 8, kExpWarps = 8;
+constexpr int kSideWarps = kExpWarps / 2;  // expanders of K, and of V
 constexpr int kMmaWarp = kSoftWarps + kExpWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kTcThreads = 32 * (kSoftWarps + kExpWarps + 4);  // four whole warpgroups
+constexpr int kTcThreads = 32 * (kSoftWarps + kExpWarps + 4);  // five whole warpgroups
+// Registers of a thread: at the launch (what 640 threads may have), then by role. A role's
+// setmaxnreg waits for registers that others gave back, so the shares must not exceed the launch's.
+constexpr int kLaunchRegs = 96, kSoftRegs = 144, kExpRegs = 64, kLastRegs = 64;
+static_assert(32 * (kSoftWarps * kSoftRegs + kExpWarps * kExpRegs + 4 * kLastRegs) <= kTcThreads * kLaunchRegs, "registers");
+
 constexpr int kPlanThreads = 1024;
-constexpr int kStartCost = 3;  // a row tile's start and end, in key tiles
+constexpr int kStartCost = 6;  // a row tile's start and end, in key tiles
 
 __host__ __device__ constexpr int key_tile(int D) { return D == 256 ? 64 : 128; }
 constexpr int kTcStages = 2;   // expanded tiles of K, and of V
@@ -179,8 +186,6 @@ MOE_DEV uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// The block is launched with 128 registers a thread (65536): the 256 softmax threads take 168,
-// the 128 expander threads 96 and the last warpgroup 80, which adds up to the same.
 template <int N>
 MOE_DEV void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -289,10 +294,12 @@ struct Walk {
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
   constexpr int KT = key_tile(D), NS = kTcStages;
-  constexpr int HK = KT / 2;                 // keys of a softmax thread
   constexpr uint32_t kTileBytes = KT * D * 2;
-  constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2, kP = kS + KT;
-  static_assert(kP + KT <= 512, "TMEM columns");
+  constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2;
+  // P has columns of its own where there is room, else it overwrites the scores it comes from
+  constexpr bool kOwnP = kS + 2 * KT + KT / 2 <= 512;
+  constexpr uint32_t kP = kOwnP ? kS + 2 * KT : kS;
+  static_assert(kS + 2 * KT <= 512, "TMEM columns");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* s_k = smem;
@@ -301,29 +308,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
   __shared__ uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   __shared__ uint32_t s_bad[kRawSlots];  // groups of 16 keys whose page number is outside the cache
   __shared__ uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  __shared__ uint64_t q_full, s_full, s_empty, p_full[2], pv_done[2], drained;
+  __shared__ uint64_t q_full, s_full[2], p_full[2], pv_done[2], m_full[4], drained;
   __shared__ uint32_t s_tmem;
   __shared__ Patience s_wait;
-  __shared__ float s_x[2][kRows];
+  __shared__ float s_x[2][kRows], s_m[kRows];
   __shared__ int s_e[2][kRows];
   __shared__ int s_idx;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&k_full[s], kExpWarps);
+      mbar_init(&k_full[s], kSideWarps);
       mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], kExpWarps);
+      mbar_init(&v_full[s], kSideWarps);
       mbar_init(&v_empty[s], 1);
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kExpWarps);
+      mbar_init(&raw_empty[i], kSideWarps);
     }
     mbar_init(&q_full, kSoftWarps);
-    mbar_init(&s_full, 1);
-    mbar_init(&s_empty, kSoftWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&m_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kSoftWarps / 2);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drained, 1);
@@ -370,8 +377,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
-    more_registers<168>();
-    const int half = warp >> 2, quarter = warp & 3;
+    more_registers<kSoftRegs>();
+    const int half = warp >> 2, quarter = warp & 3;  // half: the group, and its half of Q and O
     const int row = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t tc = 0;  // key tiles so far
@@ -425,85 +432,106 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       // keys that every row of the tile sees
       const int first_tok = run.tile * kRows / a.G;
       const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
+      const uint32_t tc_end = tc + (uint32_t)(run.u1 - run.u0);
       float m = kNoMax;
       uint64_t l2 = pack2(0.0f, 0.0f);
       const uint64_t fac2 = pack2(fac, fac);
+      auto take = [&](float top) {  // a new maximum in use
+        const float fix = ex2(m - top);
+        float a0, a1;
+        unpack2(l2, a0, a1);
+        l2 = pack2(a0 * fix, a1 * fix);
+        m = top;
+        return fix;
+      };
       for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        ok = __all_sync(0xffffffffu, wait_soon(&s_full, tc & 1, &s_wait, a.status));
+        if ((tc & 1) != (uint32_t)half) continue;  // the other group's
+        const uint32_t ts = tl + kS + half * KT;
+        const bool edge = u * KT + KT > lim_min;
+        ok = __all_sync(0xffffffffu, wait_soon(&s_full[half], (tc >> 1) & 1, &s_wait, a.status));
+        if (!ok) break;
         tc_fence_after();
-        uint32_t s[HK];
+        uint32_t s[64];
+        auto scores = [&](int c) {
+          tmem_ld32(ts + c, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+          tmem_ld32(ts + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+          tmem_ld_wait();
+          if (edge) {
 #pragma unroll
-        for (int i = 0; i < HK / 32; ++i)
-          tmem_ld32(tl + kS + half * HK + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * i]));
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty);
-        const int k0 = u * KT + half * HK;
-        if (u * KT + KT > lim_min) {
+            for (int i = 0; i < 64; ++i)
+              if (u * KT + c + i >= lim) s[i] = 0xff800000u;
+          }
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < KT; c += 64) {
+          scores(c);
 #pragma unroll
-          for (int i = 0; i < HK; ++i)
-            if (k0 + i >= lim) s[i] = 0xff800000u;
+          for (int i = 0; i < 64; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
         }
-        float mx = __uint_as_float(s[0]);
-#pragma unroll
-        for (int i = 1; i < HK; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
         mx *= fac;
-        const bool first = u == run.u0;
-        if (bar_or(1, kSoftWarps * 32, mx > m + kRaise || !ok)) {
-          s_x[half][row] = mx;
-          if (bar_or(2, kSoftWarps * 32, !ok)) {
-            ok = false;
-            break;
-          }
-          const float top = fmaxf(fmaxf(s_x[0][row], s_x[1][row]), m);
-          if (!first) {
-            const float fix = ex2(m - top);
-            float a0, a1;
-            unpack2(l2, a0, a1);
-            l2 = pack2(a0 * fix, a1 * fix);
-            ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
+        if (u > run.u0) {  // the maximum that the last tile used
+          ok = __all_sync(0xffffffffu, wait_soon(&m_full[quarter], (tc - 1) & 1, &s_wait, a.status));
+          if (!ok) break;
+          const float last = s_m[row];
+          if (last != m) take(last);
+        }
+        if (__any_sync(0xffffffffu, mx > m + kRaise)) {
+          const float fix = take(fmaxf(mx, m));
+          if (u > run.u0) {
+            ok = __all_sync(0xffffffffu, wait_soon(&pv_done[half ^ 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
+            if (!ok) break;
             tc_fence_after();
-            if (ok) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tl + kO + c, o);
+              tmem_ld_wait();
 #pragma unroll
-              for (int c = 0; c < D / 2; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tl + kO + half * (D / 2) + c, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-                tmem_st32(tl + kO + half * (D / 2) + c, o);
-              }
-              tmem_st_wait();
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+              tmem_st32(tl + kO + c, o);
             }
+            tmem_st_wait();
           }
-          m = top;
-          bar_or(1, kSoftWarps * 32, false);  // s_x is free again
         }
+        s_m[row] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m_full[quarter]);
         const uint64_t nm2 = pack2(-m, -m);
-        uint32_t p[HK / 2];
-#pragma unroll
-        for (int i = 0; i < HK / 2; ++i) {
-          const uint64_t x = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), fac2, nm2);
-          float x0, x1;
-          unpack2(x, x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          l2 = add2(l2, pack2(x0, x1));
-          p[i] = pack_f16(x0, x1);
+        const uint32_t tp = tl + kP + (kOwnP ? 0 : half * KT);
+        if (kOwnP && tc > 0) {  // the product of the tile before has read P
+          ok = __all_sync(0xffffffffu, wait_soon(&pv_done[half ^ 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
+          if (!ok) break;
+          tc_fence_after();
         }
-        if (tc >= 2)  // the product that read this P buffer two tiles ago
-          ok = __all_sync(0xffffffffu, wait_soon(&pv_done[tc & 1], ((tc >> 1) - 1) & 1, &s_wait, a.status)) && ok;
-        const uint32_t tp = tl + kP + (tc & 1) * (KT / 2) + half * (HK / 2);
-        tc_fence_after();
+#pragma unroll 1
+        for (int c = KT - 64; c >= 0; c -= 64) {  // the last scores are still in registers
+          if (c < KT - 64) scores(c);
 #pragma unroll
-        for (int i = 0; i < HK / 32; ++i) tmem_st16(tp + 16 * i, &p[16 * i]);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
+              float x0, x1;
+              unpack2(x, x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              l2 = add2(l2, pack2(x0, x1));
+              p[i] = pack_f16(x0, x1);
+            }
+            tmem_st16(tp + c / 2 + 16 * q, p);
+          }
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tc & 1]);
+        if (lane == 0) mbar_arrive(&p_full[half]);
       }
       // ---- the run's result
+      tc = tc_end;
+      if (ok) ok = __all_sync(0xffffffffu, wait_soon(&m_full[quarter], (tc - 1) & 1, &s_wait, a.status));
+      if (ok && s_m[row] != m) take(s_m[row]);
       float l0, l1;
       unpack2(l2, l0, l1);
       s_x[half][row] = l0 + l1;
@@ -563,78 +591,73 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
     }
   } else if (warp < kMmaWarp) {
     // ================================================================ expanders
-    // 32 elements (16 bytes of codes) a lane and step, lanes side by side in the raw tile. The
-    // four 16-byte stores of a lane go out in an order that depends on its place in the row, so
-    // that 8 lanes always fall into 8 different places of the swizzle.
-    fewer_registers<96>();
-    constexpr int P = D / 32;                 // lanes of a row
-    constexpr int STEPS = KT * P / (32 * kExpWarps);
-    const int pw = warp - kSoftWarps;
-    uint32_t n_raw = 0;
+    // 16 elements (8 bytes of codes, one scale) a lane and step, lanes side by side in the raw
+    // tile. A step is a whole number of 8 rows on, so a lane keeps its place in the swizzle; of its
+    // two 16-byte stores, lanes that would meet in a bank take the second one first. Half of the
+    // warps take K, the others V: a tile's way through shared memory is mostly latency.
+    fewer_registers<kExpRegs>();
+    constexpr int P = D / 16;                 // lanes of a row
+    constexpr int STEPS = KT * P / (32 * kSideWarps), ROWS = 32 / P * kSideWarps;  // rows of a step
+    static_assert(ROWS % 8 == 0, "a lane keeps its row modulo 8");
+    const int pw = (warp - kSoftWarps) % kSideWarps;
+    const bool is_v = warp >= kSoftWarps + kSideWarps;
+    const int row0 = (pw * 32 + lane) / P, part = lane % P;
+    const bool swap = D >= 128 && (part & 4);
+    const uint32_t off0 = (part >> 2) * (KT * 128) + row0 * 128 + (((((part & 3) << 1) | (swap ? 1 : 0)) ^ (row0 & 7)) << 4);
+    const uint32_t off1 = off0 ^ 16;
+    uint64_t* t_full = is_v ? v_full : k_full;
+    uint64_t* t_empty = is_v ? v_empty : k_empty;
+    uint32_t tc = 0;
     bool ok = true;
     Run run;
     while (ok && walk.next(&run)) {
       const int ctx = load_seq(a, run.b).ctx;
 #pragma unroll 1
-      for (int i = 2 * run.u0; i < 2 * run.u1; ++i, ++n_raw) {  // K and V of each tile in turn
-        const bool is_v = i & 1;
-        const uint32_t slot = n_raw % kRawSlots, s = (n_raw >> 1) % NS;
+      for (int u = run.u0; u < run.u1; ++u, ++tc) {
+        const uint32_t n_raw = 2 * tc + (is_v ? 1 : 0), slot = n_raw % kRawSlots, s = tc % NS;
         ok = __all_sync(0xffffffffu, wait_soon(&raw_full[slot], (n_raw / kRawSlots) & 1, &s_wait, a.status)) &&
-             __all_sync(0xffffffffu, wait_soon(is_v ? &v_empty[s] : &k_empty[s], ((n_raw / (2 * NS)) & 1) ^ 1, &s_wait,
-                                               a.status));
+             __all_sync(0xffffffffu, wait_soon(&t_empty[s], ((tc / NS) & 1) ^ 1, &s_wait, a.status));
         if (!ok) break;
         const uint8_t* raw = s_raw + slot * raw_bytes(D);
         uint8_t* tile = (is_v ? s_v : s_k) + s * kTileBytes;
         const uint32_t bad = s_bad[slot];
-        const int left = ctx - (i >> 1) * KT;
-        uint4 codes[STEPS];
+        const int left = ctx - u * KT;
+        uint2 codes[STEPS];
         uint32_t scales[STEPS];
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
-          const int unit = (step * kExpWarps + pw) * 32 + lane;
-          codes[step] = reinterpret_cast<const uint4*>(raw)[unit];
-          scales[step] = reinterpret_cast<const uint16_t*>(raw + KT * (D / 2))[unit];
+          codes[step] = reinterpret_cast<const uint2*>(raw)[(step * kSideWarps + pw) * 32 + lane];
+          scales[step] = (raw + KT * (D / 2))[(step * kSideWarps + pw) * 32 + lane];
+        }
+        if (bad || left < KT) {  // keys past the end, and pages outside the cache, count as zeros
+#pragma unroll
+          for (int step = 0; step < STEPS; ++step) {
+            const int row = row0 + step * ROWS;
+            if (row >= left || ((bad >> (row / 16)) & 1u)) scales[step] = 0u;
+          }
         }
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
-          const int unit = (step * kExpWarps + pw) * 32 + lane, row = unit / P, part = unit % P;
-          // keys past the end, and pages outside the cache, count as zeros
-          const uint32_t sc2 = row >= left || ((bad >> (row / 16)) & 1u) ? 0u : scales[step];
-          uint8_t* dst = tile + (part >> 1) * (KT * 128) + row * 128;
-          uint32_t w0 = codes[step].x, w1 = codes[step].y, w2 = codes[step].z, w3 = codes[step].w;
-          uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(sc2, 0, 0x0000)), s1 = e4m3x2_to_f16x2(__byte_perm(sc2, 0, 0x0011));
-          // turn: 2 bits for the 4 pairs of lanes of a row of 8, 1 (as 0 or 2) for 2 pairs of 4
-          const int turn = D == 256 ? part >> 1 : D == 128 ? part & 2 : 0;
-          if (turn & 2) {
-            uint32_t x = w0; w0 = w2; w2 = x;
-            x = w1; w1 = w3; w3 = x;
-            x = s0; s0 = s1; s1 = x;
-          }
-          if (turn & 1) {
-            uint32_t x = w0; w0 = w1; w1 = x;
-            x = w2; w2 = w3; w3 = x;
-          }
-          const uint32_t w[4] = {w0, w1, w2, w3};
-          const int chunk = ((part & 1) * 4 + turn) ^ (row & 7);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t f[4];
-            e2m1x8_to_f16x2x4(w[j], f);
-            const uint32_t sc = j < 2 ? s0 : s1;
-            *reinterpret_cast<uint4*>(dst + ((chunk ^ j) << 4)) =
-                make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
-          }
+          const uint32_t w0 = swap ? codes[step].y : codes[step].x, w1 = swap ? codes[step].x : codes[step].y;
+          const uint32_t sc = e4m3x2_to_f16x2(scales[step] * 0x0101u);
+          uint32_t f[4];
+          e2m1x8_to_f16x2x4(w0, f);
+          *reinterpret_cast<uint4*>(tile + off0 + step * (ROWS * 128)) =
+              make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+          e2m1x8_to_f16x2x4(w1, f);
+          *reinterpret_cast<uint4*>(tile + off1 + step * (ROWS * 128)) =
+              make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_empty[slot]);
-          mbar_arrive(is_v ? &v_full[s] : &k_full[s]);
+          mbar_arrive(&t_full[s]);
         }
       }
     }
   } else {
-    fewer_registers<80>();
+    fewer_registers<kLastRegs>();
     if (warp == kLoadWarp) {
       // ================================================================ loader
       // a lane copies one page's part of the tile: at most KT / 16 pages
@@ -712,16 +735,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
           if (j < n) {  // S = Q K^T of tile j
             const uint32_t t = tc + j, s = t % NS;
             wait(&k_full[s], (t / NS) & 1);
-            wait(&s_empty, (t & 1) ^ 1);
+            // (its scores have been read: PV(t - 2) went out before)
+            if (!kOwnP && t >= 2) wait(&pv_done[t & 1], ((t >> 1) - 1) & 1);  // P of tile t - 2 has been read
             if (!ok) break;
             tc_fence_after();
             const uint64_t desc = desc_k + s * (kTileBytes >> 4);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                mma_f16_ts(tmem + kS, tmem + kQ + 8 * kk, desc + (((kk / 4) * (KT * 128) + (kk % 4) * 32) >> 4), idesc_qk,
+                mma_f16_ts(tmem + kS + (t & 1) * KT, tmem + kQ + 8 * kk, desc + (((kk / 4) * (KT * 128) + (kk % 4) * 32) >> 4), idesc_qk,
                            kk ? 1u : 0u);
-              mma_commit(&s_full);
+              mma_commit(&s_full[t & 1]);
               mma_commit(&k_empty[s]);
             }
             __syncwarp();
@@ -733,7 +757,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
             if (!ok) break;
             tc_fence_after();
             const uint64_t desc = desc_v + s * (kTileBytes >> 4);
-            const uint32_t p = tmem + kP + (t & 1) * (KT / 2), add = j > 1 ? 1u : 0u;
+            const uint32_t p = tmem + kP + (kOwnP ? 0 : (t & 1) * KT), add = j > 1 ? 1u : 0u;
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < KT / 16; ++kk)
@@ -820,11 +844,19 @@ size_t kv_attn_tc_tiles_bytes(int64_t T, int n_seqs, int G) {
 
 cudaError_t set_wait_limit_kv_attn_tc(unsigned long long ns) { return set_wait_limit_here(ns); }
 
+template <int D>
+static cudaError_t attributes_tc() {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, kv_attn_tc_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;  // the roles' shares would not add up
+  return cudaFuncSetAttribute(kv_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem(D));
+}
+
 cudaError_t init_kv_attn_tc_attributes() {
-  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_tc_kernel<64>, at, tc_smem(64));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_attn_tc_kernel<128>, at, tc_smem(128));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_attn_tc_kernel<256>, at, tc_smem(256));
+  cudaError_t e = attributes_tc<64>();
+  if (e == cudaSuccess) e = attributes_tc<128>();
+  if (e == cudaSuccess) e = attributes_tc<256>();
   return e;
 }
 
