@@ -2,23 +2,20 @@
 // prompts): out = softmax(scale q K^T) V, both products on the tcgen05 tensor cores.
 //
 // A block takes tiles of 128 query rows of one key head (row = token * G + head of the group, so
-// the G heads that share keys share the expanded keys too) and walks over the keys KT at a time:
+// the G heads that share keys share the expanded keys too) and walks over the keys KT at a time (128; 64 for D = 256, whose
+// O and Q leave TMEM no room for more):
 //   loader warp: a tile's codes and scales by bulk copies (a page's rows of one head are
-//     contiguous) into a ring of raw tiles, several ahead.
-//   expander warps: raw tiles to float16 (exact: 2 + 4 significant bits) in the 128-byte
+//     contiguous) into a ring of raw slots, several ahead.
+//   expander warps: raw slots to float16 (exact: 2 + 4 significant bits) in the 128-byte
 //     swizzle. K rows are the K-major B operand of S = Q K^T; V rows, stored the same way, are
 //     the MN-major B operand of O += P V, so neither is transposed.
-//   MMA warp: S = Q K^T with Q (float16, scaled by a power of two per row) as the A operand in
-//     TMEM, O += P V with P in TMEM. With both A operands in TMEM a product reads shared memory
-//     at half the rate that two shared operands would, which leaves room for the writes of the
-//     expanded tiles (a D = 256 tile is written once per 128 rows).
-//   softmax warps: two groups of 128 threads, a thread a row, that take the key tiles in turn,
-//     so that one group's exponentials (the busiest unit, 16 a cycle) run beside the other's
-//     maxima and copies. P overwrites S in TMEM. The maximum in use passes from tile to tile
-//     through shared memory; O is rescaled only when a row's maximum rises by more than 2^8 over
-//     it; the weights are below 2^8 in float16, the sums in float32.
-// The order of the tensor pipe is QK(j), PV(j-1), QK(j+1), ... TMEM: O [0, D), Q [D, 1.5 D), two
-// S / P buffers of KT columns.
+//   MMA warp: S = Q K^T, then O += P V of the tile before. Q (float16, scaled by a power of two
+//     per row) and P are A operands in TMEM: a product with two operands in shared memory reads
+//     it at its full rate, beside the writes of the expanded tiles.
+//   softmax warps: two threads a row, each half of the keys. They copy S to registers first, so
+//     the next Q K^T can overwrite it while they work, and a tile's softmax has a PV and a QK of
+//     time. O is rescaled only when a row's maximum rises by more than 2^8 over the one in use;
+//     the weights are below 2^8 in float16, the sums in float32.
 //
 // Tiles have different numbers of keys (causal, ragged), so the work (key tiles, plus a few for
 // each row tile's start and end) is dealt to the blocks in equal contiguous runs; a plan kernel
@@ -34,7 +31,6 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kSoftWarps = 8, kExpWarps = 8;
-constexpr int kSideWarps = kExpWarps / 2;  // expanders of K, and of V
 constexpr int kMmaWarp = kSoftWarps + kExpWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kTcThreads = 32 * (kSoftWarps + kExpWarps + 4);  // five whole warpgroups
 // Registers of a thread: at the launch (what 640 threads may have), then by role. A role's
@@ -46,8 +42,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kStartCost = 6;  // a row tile's start and end, in key tiles
 
 __host__ __device__ constexpr int key_tile(int D) { return D == 256 ? 64 : 128; }
-constexpr int kTcStages = 2;   // expanded tiles of K, and of V
-constexpr int kRawSlots = 8;   // raw tiles, K and V in turn
+constexpr int kTcStages = 2;  // expanded tiles of K, and of V
+constexpr int kRawSlots = 8;  // raw tiles, K and V in turn
 __host__ __device__ constexpr int raw_bytes(int D) { return key_tile(D) * (D / 2 + D / 16); }
 constexpr int tc_smem(int D) { return 2 * kTcStages * key_tile(D) * D * 2 + kRawSlots * raw_bytes(D) + 1024; }
 
@@ -254,6 +250,13 @@ MOE_DEV bool wait_soon(uint64_t* bar, uint32_t parity, Patience* w, int32_t* sta
   return true;
 }
 
+// Waits for two barriers at once, every other lane for the second (a wait that is over at once
+// still costs the round trip). For a whole warp; the same answer in all lanes.
+MOE_DEV bool wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1, Patience* w, int32_t* status) {
+  const bool odd = threadIdx.x & 1;
+  return __all_sync(0xffffffffu, wait_soon(odd ? bar1 : bar0, odd ? parity1 : parity0, w, status));
+}
+
 // A run of key tiles of one row tile.
 struct Run {
   int b, h, tile, u0, u1, n_units;
@@ -293,44 +296,43 @@ struct Walk {
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
-  constexpr int KT = key_tile(D), NS = kTcStages;
+  constexpr int KT = key_tile(D), HK = KT / 2, NS = kTcStages, RAW = kRawSlots;
+  constexpr int EW = kExpWarps / 2;  // expander warps of K, and of V
   constexpr uint32_t kTileBytes = KT * D * 2;
-  constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2;
-  // P has columns of its own where there is room, else it overwrites the scores it comes from
-  constexpr bool kOwnP = kS + 2 * KT + KT / 2 <= 512;
-  constexpr uint32_t kP = kOwnP ? kS + 2 * KT : kS;
-  static_assert(kS + 2 * KT <= 512, "TMEM columns");
+  // TMEM columns: O, Q, S, two P
+  constexpr uint32_t kO = 0, kQ = D, kS = kQ + D / 2, kP = kS + KT;
+  static_assert(kP + KT <= 512, "TMEM columns");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* s_k = smem;
-  uint8_t* s_v = smem + NS * kTileBytes;
-  uint8_t* s_raw = smem + 2 * NS * kTileBytes;
-  __shared__ uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
-  __shared__ uint32_t s_bad[kRawSlots];  // groups of 16 keys whose page number is outside the cache
+  uint8_t* s_v = s_k + NS * kTileBytes;
+  uint8_t* s_raw = s_v + NS * kTileBytes;
+  __shared__ uint64_t raw_full[RAW], raw_empty[RAW];
+  __shared__ uint32_t s_bad[RAW];  // groups of 16 keys whose page number is outside the cache
   __shared__ uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  __shared__ uint64_t q_full, s_full[2], p_full[2], pv_done[2], m_full[4], drained;
+  __shared__ uint64_t q_full, s_full, s_empty, p_full[2], pv_done[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ Patience s_wait;
-  __shared__ float s_x[2][kRows], s_m[kRows];
+  __shared__ float s_x[2][kRows];
   __shared__ int s_e[2][kRows];
   __shared__ int s_idx;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&k_full[s], kSideWarps);
+      mbar_init(&k_full[s], EW);
       mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], kSideWarps);
+      mbar_init(&v_full[s], EW);
       mbar_init(&v_empty[s], 1);
     }
-    for (int i = 0; i < kRawSlots; ++i) {
+    for (int i = 0; i < RAW; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kSideWarps);
+      mbar_init(&raw_empty[i], EW);
     }
     mbar_init(&q_full, kSoftWarps);
-    for (int i = 0; i < 4; ++i) mbar_init(&m_full[i], 1);
+    mbar_init(&s_full, 1);
+    mbar_init(&s_empty, kSoftWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoftWarps / 2);
+      mbar_init(&p_full[i], kSoftWarps);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drained, 1);
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
   if (warp < kSoftWarps) {
     // ================================================================ softmax
     more_registers<kSoftRegs>();
-    const int half = warp >> 2, quarter = warp & 3;  // half: the group, and its half of Q and O
+    const int half = warp >> 2, quarter = warp & 3;  // half of the keys, of Q and of O
     const int row = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t tc = 0;  // key tiles so far
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
           mx = __vmaxu2(mx, raw[i].w & 0x7FFF7FFFu);
         }
         s_e[half][row] = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;
-        named_bar_sync(1, kSoftWarps * 32);
+        named_bar_sync(5, kSoftWarps * 32);
         const int e = max(max(s_e[0][row], s_e[1][row]), -100);
         // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
         const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
@@ -432,112 +434,94 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       // keys that every row of the tile sees
       const int first_tok = run.tile * kRows / a.G;
       const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
-      const uint32_t tc_end = tc + (uint32_t)(run.u1 - run.u0);
       float m = kNoMax;
       uint64_t l2 = pack2(0.0f, 0.0f);
       const uint64_t fac2 = pack2(fac, fac);
-      auto take = [&](float top) {  // a new maximum in use
-        const float fix = ex2(m - top);
-        float a0, a1;
-        unpack2(l2, a0, a1);
-        l2 = pack2(a0 * fix, a1 * fix);
-        m = top;
-        return fix;
-      };
       for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        if ((tc & 1) != (uint32_t)half) continue;  // the other group's
-        const uint32_t ts = tl + kS + half * KT;
-        const bool edge = u * KT + KT > lim_min;
-        ok = __all_sync(0xffffffffu, wait_soon(&s_full[half], (tc >> 1) & 1, &s_wait, a.status));
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, wait_soon(&s_full, tc & 1, &s_wait, a.status)) && ok;
         tc_fence_after();
-        uint32_t s[64];
-        auto scores = [&](int c) {
-          tmem_ld32(ts + c, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-          tmem_ld32(ts + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-          tmem_ld_wait();
-          if (edge) {
+        uint32_t s[HK];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (u * KT + c + i >= lim) s[i] = 0xff800000u;
-          }
-        };
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < KT; c += 64) {
-          scores(c);
-#pragma unroll
-          for (int i = 0; i < 64; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-        }
-        mx *= fac;
-        if (u > run.u0) {  // the maximum that the last tile used
-          ok = __all_sync(0xffffffffu, wait_soon(&m_full[quarter], (tc - 1) & 1, &s_wait, a.status));
-          if (!ok) break;
-          const float last = s_m[row];
-          if (last != m) take(last);
-        }
-        if (__any_sync(0xffffffffu, mx > m + kRaise)) {
-          const float fix = take(fmaxf(mx, m));
-          if (u > run.u0) {
-            ok = __all_sync(0xffffffffu, wait_soon(&pv_done[half ^ 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tl + kO + c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-              tmem_st32(tl + kO + c, o);
-            }
-            tmem_st_wait();
-          }
-        }
-        s_m[row] = m;
+        for (int i = 0; i < HK; i += 32) tmem_ld32(tl + kS + half * HK + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+        tmem_ld_wait();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m_full[quarter]);
-        const uint64_t nm2 = pack2(-m, -m);
-        const uint32_t tp = tl + kP + (kOwnP ? 0 : half * KT);
-        if (kOwnP && tc > 0) {  // the product of the tile before has read P
-          ok = __all_sync(0xffffffffu, wait_soon(&pv_done[half ^ 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
-          if (!ok) break;
+        if (lane == 0) mbar_arrive(&s_empty);
+        if (u * KT + KT > lim_min) {
+          const int left = lim - u * KT - half * HK;
+#pragma unroll
+          for (int i = 0; i < HK; ++i)
+            if (i >= left) s[i] = 0xff800000u;
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < HK; i += 2)
+          mx4[(i / 2) & 3] = fmaxf(mx4[(i / 2) & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
+        // the two warps of these 32 rows decide together
+        if (bar_or(1 + quarter, 64, mx > m + kRaise || !ok)) {
+          s_x[half][row] = mx;
+          if (bar_or(1 + quarter, 64, !ok)) {
+            ok = false;
+            break;
+          }
+          const float top = fmaxf(fmaxf(s_x[0][row], s_x[1][row]), m);
+          if (u > run.u0) {
+            const float fix = ex2(m - top);
+            float a0, a1;
+            unpack2(l2, a0, a1);
+            l2 = pack2(a0 * fix, a1 * fix);
+            ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
+            tc_fence_after();
+            if (ok) {
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tl + kO + half * (D / 2) + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+                tmem_st32(tl + kO + half * (D / 2) + c, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          m = top;
+          bar_or(1 + quarter, 64, false);  // s_x is free again
+        }
+        if (tc >= 2) {  // the product that last read these columns of P
+          ok = __all_sync(0xffffffffu, wait_soon(&pv_done[tc & 1], ((tc >> 1) - 1) & 1, &s_wait, a.status)) && ok;
           tc_fence_after();
         }
-#pragma unroll 1
-        for (int c = KT - 64; c >= 0; c -= 64) {  // the last scores are still in registers
-          if (c < KT - 64) scores(c);
+        const uint64_t nm2 = pack2(-m, -m);
+        const uint32_t tp = tl + kP + (tc & 1) * (KT / 2) + half * (HK / 2);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t p[16];
+        for (int q = 0; q < HK / 32; ++q) {
+          uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
-              float x0, x1;
-              unpack2(x, x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              l2 = add2(l2, pack2(x0, x1));
-              p[i] = pack_f16(x0, x1);
-            }
-            tmem_st16(tp + c / 2 + 16 * q, p);
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
+            float x0, x1;
+            unpack2(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            l2 = add2(l2, pack2(x0, x1));
+            p[i] = pack_f16(x0, x1);
           }
+          tmem_st16(tp + 16 * q, p);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[half]);
+        if (lane == 0) mbar_arrive(&p_full[tc & 1]);
       }
       // ---- the run's result
-      tc = tc_end;
-      if (ok) ok = __all_sync(0xffffffffu, wait_soon(&m_full[quarter], (tc - 1) & 1, &s_wait, a.status));
-      if (ok && s_m[row] != m) take(s_m[row]);
       float l0, l1;
       unpack2(l2, l0, l1);
       s_x[half][row] = l0 + l1;
       if (ok) ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
       tc_fence_after();
-      if (bar_or(1, kSoftWarps * 32, !ok)) break;
+      if (bar_or(5, kSoftWarps * 32, !ok)) break;
       const float ll = s_x[0][row] + s_x[1][row];
       const bool whole = run.u0 == 0 && run.u1 == run.n_units;
       const float vts = a.cache.v_ts ? a.cache.v_ts[run.h] : 1.0f;
@@ -587,26 +571,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
         a.meta[blockIdx.x] = make_int4(run.b, run.h, run.tile * kRows, last);
       }
       tc_fence_before();
-      named_bar_sync(1, kSoftWarps * 32);  // s_x and s_e are free again, O has been read
+      named_bar_sync(5, kSoftWarps * 32);  // s_x and s_e are free again, O has been read
     }
   } else if (warp < kMmaWarp) {
     // ================================================================ expanders
     // 16 elements (8 bytes of codes, one scale) a lane and step, lanes side by side in the raw
-    // tile. A step is a whole number of 8 rows on, so a lane keeps its place in the swizzle; of its
-    // two 16-byte stores, lanes that would meet in a bank take the second one first. Half of the
-    // warps take K, the others V: a tile's way through shared memory is mostly latency.
+    // slot. A step is a whole number of 8 rows on, so a lane keeps its place in the swizzle; of its
+    // two 16-byte stores, lanes that would meet in a bank take the second one first.
     fewer_registers<kExpRegs>();
     constexpr int P = D / 16;                 // lanes of a row
-    constexpr int STEPS = KT * P / (32 * kSideWarps), ROWS = 32 / P * kSideWarps;  // rows of a step
+    constexpr int STEPS = KT * P / (32 * EW), ROWS = 32 / P * EW;  // rows of a step
     static_assert(ROWS % 8 == 0, "a lane keeps its row modulo 8");
-    const int pw = (warp - kSoftWarps) % kSideWarps;
-    const bool is_v = warp >= kSoftWarps + kSideWarps;
+    const int pw = (warp - kSoftWarps) % EW;
+    const bool is_v = warp >= kSoftWarps + EW;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
     const int row0 = (pw * 32 + lane) / P, part = lane % P;
     const bool swap = D >= 128 && (part & 4);
     const uint32_t off0 = (part >> 2) * (KT * 128) + row0 * 128 + (((((part & 3) << 1) | (swap ? 1 : 0)) ^ (row0 & 7)) << 4);
     const uint32_t off1 = off0 ^ 16;
-    uint64_t* t_full = is_v ? v_full : k_full;
-    uint64_t* t_empty = is_v ? v_empty : k_empty;
     uint32_t tc = 0;
     bool ok = true;
     Run run;
@@ -614,20 +597,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       const int ctx = load_seq(a, run.b).ctx;
 #pragma unroll 1
       for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        const uint32_t n_raw = 2 * tc + (is_v ? 1 : 0), slot = n_raw % kRawSlots, s = tc % NS;
-        ok = __all_sync(0xffffffffu, wait_soon(&raw_full[slot], (n_raw / kRawSlots) & 1, &s_wait, a.status)) &&
-             __all_sync(0xffffffffu, wait_soon(&t_empty[s], ((tc / NS) & 1) ^ 1, &s_wait, a.status));
+        const uint32_t n_raw = 2 * tc + (is_v ? 1 : 0), slot = n_raw % RAW, s = tc % NS;
+        ok = wait_both(&raw_full[slot], (n_raw / RAW) & 1, &empty[s], ((tc / NS) & 1) ^ 1, &s_wait, a.status);
         if (!ok) break;
         const uint8_t* raw = s_raw + slot * raw_bytes(D);
-        uint8_t* tile = (is_v ? s_v : s_k) + s * kTileBytes;
         const uint32_t bad = s_bad[slot];
         const int left = ctx - u * KT;
         uint2 codes[STEPS];
         uint32_t scales[STEPS];
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
-          codes[step] = reinterpret_cast<const uint2*>(raw)[(step * kSideWarps + pw) * 32 + lane];
-          scales[step] = (raw + KT * (D / 2))[(step * kSideWarps + pw) * 32 + lane];
+          codes[step] = reinterpret_cast<const uint2*>(raw)[(step * EW + pw) * 32 + lane];
+          scales[step] = (raw + KT * (D / 2))[(step * EW + pw) * 32 + lane];
         }
         if (bad || left < KT) {  // keys past the end, and pages outside the cache, count as zeros
 #pragma unroll
@@ -636,23 +617,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
             if (row >= left || ((bad >> (row / 16)) & 1u)) scales[step] = 0u;
           }
         }
+        uint8_t* dst = (is_v ? s_v : s_k) + s * kTileBytes;
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
           const uint32_t w0 = swap ? codes[step].y : codes[step].x, w1 = swap ? codes[step].x : codes[step].y;
           const uint32_t sc = e4m3x2_to_f16x2(scales[step] * 0x0101u);
           uint32_t f[4];
           e2m1x8_to_f16x2x4(w0, f);
-          *reinterpret_cast<uint4*>(tile + off0 + step * (ROWS * 128)) =
+          *reinterpret_cast<uint4*>(dst + off0 + step * (ROWS * 128)) =
               make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
           e2m1x8_to_f16x2x4(w1, f);
-          *reinterpret_cast<uint4*>(tile + off1 + step * (ROWS * 128)) =
+          *reinterpret_cast<uint4*>(dst + off1 + step * (ROWS * 128)) =
               make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_empty[slot]);
-          mbar_arrive(&t_full[s]);
+          mbar_arrive(&full[s]);
         }
       }
     }
@@ -666,7 +648,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       Run run;
       const int ps = a.cache.page_size;
       const int rows = min(ps, KT);               // of a copy
-      const int copies = KT / rows;
+      const int copies = KT / rows;               // of a slot
       while (ok && walk.next(&run)) {
         const int ctx = load_seq(a, run.b).ctx;
         const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
@@ -681,29 +663,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
           const bool wanted = lane < copies && t < ctx;
           const bool good = wanted && page >= 0 && page < a.cache.n_pages;
           if (wanted && !good) atomicExch(a.status, kStatusInvalid);
-          // a copy of `rows` keys is rows / 16 groups of 16
-          uint32_t bad = 0;
-          const uint32_t lanes = __ballot_sync(0xffffffffu, wanted && !good);
-          for (int i = 0; i < copies; ++i)
-            if ((lanes >> i) & 1u) bad |= ((1u << (rows / 16)) - 1u) << (i * (rows / 16));
-          const uint32_t n_good = __popc(__ballot_sync(0xffffffffu, good));
+          const uint32_t bads = __ballot_sync(0xffffffffu, wanted && !good), goods = __ballot_sync(0xffffffffu, good);
           const int64_t row = ((int64_t)page * a.cache.Hkv + run.h) * ps + (t & (ps - 1));
-#pragma unroll
-          for (int kv = 0; kv < 2 && ok; ++kv, ++n_raw) {
-            const uint32_t slot = n_raw % kRawSlots;
-            ok = __all_sync(0xffffffffu, wait_soon(&raw_empty[slot], ((n_raw / kRawSlots) & 1) ^ 1, &s_wait, a.status));
+          uint32_t bad = 0;  // a copy of `rows` keys is rows / 16 groups of 16
+          for (int j = 0; bads && j < copies; ++j)
+            if ((bads >> j) & 1u) bad |= ((1u << (rows / 16)) - 1u) << (j * (rows / 16));
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i, ++n_raw) {  // K, then V
+            const uint32_t slot = n_raw % RAW;
+            ok = __all_sync(0xffffffffu, wait_soon(&raw_empty[slot], ((n_raw / RAW) & 1) ^ 1, &s_wait, a.status));
             if (!ok) break;
             uint8_t* raw = s_raw + slot * raw_bytes(D);
             if (lane == 0) {
               s_bad[slot] = bad;
-              mbar_arrive_expect_tx(&raw_full[slot], n_good * rows * (D / 2 + D / 16));
+              mbar_arrive_expect_tx(&raw_full[slot], __popc(goods) * rows * (D / 2 + D / 16));
             }
             __syncwarp();
             if (good) {
-              bulk_g2s(raw + lane * rows * (D / 2), (kv ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2),
-                       rows * (D / 2), &raw_full[slot]);
-              bulk_g2s(raw + KT * (D / 2) + lane * rows * (D / 16),
-                       (kv ? a.cache.v_scales : a.cache.k_scales) + row * (D / 16), rows * (D / 16), &raw_full[slot]);
+              bulk_g2s(raw + lane * rows * (D / 2), (i ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2), rows * (D / 2),
+                       &raw_full[slot]);
+              bulk_g2s(raw + KT * (D / 2) + lane * rows * (D / 16), (i ? a.cache.v_scales : a.cache.k_scales) + row * (D / 16),
+                       rows * (D / 16), &raw_full[slot]);
             }
           }
           page = next;
@@ -711,9 +691,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
       }
       // no copy may still be landing when the block ends
       __syncwarp();
-      for (uint32_t j = n_raw > kRawSlots ? n_raw - kRawSlots : 0; j < n_raw; ++j) {
+      for (uint32_t j = n_raw > RAW ? n_raw - RAW : 0; j < n_raw; ++j) {
         volatile int no_abort = 0;
-        mbar_wait(&raw_full[j % kRawSlots], (j / kRawSlots) & 1, &no_abort, a.status);
+        mbar_wait(&raw_full[j % RAW], (j / RAW) & 1, &no_abort, a.status);
       }
     } else if (warp == kMmaWarp) {
       // ================================================================ MMA
@@ -732,32 +712,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
         ++items;
         const int n = run.u1 - run.u0;
         for (int j = 0; j <= n && ok; ++j) {
-          if (j < n) {  // S = Q K^T of tile j
+          if (j < n) {  // S = Q K^T of tile j, once the scores of the tile before have been read
             const uint32_t t = tc + j, s = t % NS;
-            wait(&k_full[s], (t / NS) & 1);
-            // (its scores have been read: PV(t - 2) went out before)
-            if (!kOwnP && t >= 2) wait(&pv_done[t & 1], ((t >> 1) - 1) & 1);  // P of tile t - 2 has been read
+            ok = ok && wait_both(&k_full[s], (t / NS) & 1, &s_empty, (t & 1) ^ 1, &s_wait, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint64_t desc = desc_k + s * (kTileBytes >> 4);
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                mma_f16_ts(tmem + kS + (t & 1) * KT, tmem + kQ + 8 * kk, desc + (((kk / 4) * (KT * 128) + (kk % 4) * 32) >> 4), idesc_qk,
-                           kk ? 1u : 0u);
-              mma_commit(&s_full[t & 1]);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk / 4) * (KT * 128) + (kk % 4) * 32) >> 4;
+                mma_f16_ts(tmem + kS, tmem + kQ + 8 * kk, desc + off, idesc_qk, kk ? 1u : 0u);
+              }
+              mma_commit(&s_full);
               mma_commit(&k_empty[s]);
             }
             __syncwarp();
           }
           if (j > 0) {  // O += P V of tile j - 1
             const uint32_t t = tc + j - 1, s = t % NS;
-            wait(&v_full[s], (t / NS) & 1);
-            wait(&p_full[t & 1], (t >> 1) & 1);
+            ok = wait_both(&p_full[t & 1], (t >> 1) & 1, &v_full[s], (t / NS) & 1, &s_wait, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint64_t desc = desc_v + s * (kTileBytes >> 4);
-            const uint32_t p = tmem + kP + (kOwnP ? 0 : (t & 1) * KT), add = j > 1 ? 1u : 0u;
+            const uint32_t p = tmem + kP + (t & 1) * (KT / 2), add = j > 1 ? 1u : 0u;
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < KT / 16; ++kk)
