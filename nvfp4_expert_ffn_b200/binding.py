@@ -346,49 +346,48 @@ class _PrepC(ctypes.Structure):
                 ("rot_dim", _I32), ("interleaved", _I32), ("rot_scale", ctypes.c_double)]
 
 
-def _need(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Optional[int]:
-    """The device pointer of a contiguous tensor of this type and shape (None in, None out)."""
+def _need(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int) -> Optional[int]:
+    """The device pointer of a contiguous tensor of this type and shape on GPU `dev` (None in,
+    None out). Calls of a few microseconds go through here: plain comparisons only."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on device {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _head_rows(t: torch.Tensor, name: str, T: int, D: int, device):
-    """Pointer and token stride of bf16 rows [T][heads][D] whose heads lie side by side."""
-    if t.dtype not in (torch.bfloat16, torch.int16) or t.dim() != 3 or t.device != device:
-        raise ValueError(f"{name} must be a bf16 tensor [T][heads][D] on {device}, got {t.dtype} "
+def _head_rows(t: torch.Tensor, name: str, T: int, D: int, dev: int):
+    """Pointer, token stride and heads of bf16 rows [T][heads][D] whose heads lie side by side."""
+    if t.dim() != 3 or (t.dtype is not torch.bfloat16 and t.dtype is not torch.int16) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor [T][heads][D] on device {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     n, heads, d = t.shape
-    s = t.stride()
-    if n != T or d != D or (d > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+    s0, s1, s2 = t.stride()
+    if n != T or d != D or s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError(f"{name} must be [{T}][heads][{D}] with contiguous heads, got {tuple(t.shape)} "
-                         f"with strides {s}")
-    return t.data_ptr(), (s[0] if n > 1 else heads * D)
+                         f"with strides {t.stride()}")
+    return t.data_ptr(), (s0 if n > 1 else heads * D), heads
 
 
-class _On:
-    """The tensors' device as the current one for a call, and the stream to use on it."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(name: str, dev: int, stream, *args) -> None:
+    """lib().<name>(*args, stream) with the tensors' device as the current one."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on device {dev}")
+        s = stream.cuda_stream
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, s)
+    if status != MOE_OK:
+        _check(name, status)
 
 
 @dataclass(frozen=True)
@@ -402,19 +401,21 @@ class KVCache:
     v_scales: torch.Tensor
     k_ts: Optional[torch.Tensor] = None  # float32 [Hkv]: static tensor scales (None: 1)
     v_ts: Optional[torch.Tensor] = None
-    _c: _CacheC = field(default=None, repr=False, compare=False)
 
     def __post_init__(self):
         if self.k_codes.dim() != 4:
             raise ValueError("k_codes must be [n_pages][Hkv][page_size][D/2]")
         n, H, ps, dh = self.k_codes.shape
-        dev, u8 = self.k_codes.device, torch.uint8
+        dev, u8 = self.k_codes.get_device(), torch.uint8
         p = [_need(self.k_codes, "k_codes", u8, (n, H, ps, dh), dev),
              _need(self.k_scales, "k_scales", u8, (n, H, ps, dh // 8), dev),
              _need(self.v_codes, "v_codes", u8, (n, H, ps, dh), dev),
              _need(self.v_scales, "v_scales", u8, (n, H, ps, dh // 8), dev),
              _need(self.k_ts, "k_ts", torch.float32, (H,), dev), _need(self.v_ts, "v_ts", torch.float32, (H,), dev)]
-        object.__setattr__(self, "_c", _CacheC(n, ps, H, 2 * dh, *p))
+        c = _CacheC(n, ps, H, 2 * dh, *p)
+        for name, value in (("n_pages", n), ("page_size", ps), ("Hkv", H), ("D", 2 * dh), ("dev", dev), ("_c", c),
+                            ("ref", ctypes.byref(c))):
+            object.__setattr__(self, name, value)
 
     @classmethod
     def allocate(cls, n_pages: int, page_size: int, Hkv: int, D: int, k_ts=None, v_ts=None, device="cuda"):
@@ -426,22 +427,6 @@ class KVCache:
     @property
     def device(self):
         return self.k_codes.device
-
-    @property
-    def D(self):
-        return self._c.D
-
-    @property
-    def Hkv(self):
-        return self._c.Hkv
-
-    @property
-    def page_size(self):
-        return self._c.page_size
-
-    @property
-    def n_pages(self):
-        return self._c.n_pages
 
 
 @dataclass(frozen=True)
@@ -455,31 +440,34 @@ class QKPrep:
     interleaved: bool = False
     rot_scale: float = 1.0
 
-    def struct(self, D: int, device) -> _PrepC:
-        f32 = torch.float32
-        half = 0 if self.inv_freq is None else self.inv_freq.numel()
-        return _PrepC(_need(self.q_weight, "q_weight", f32, (D,), device), _need(self.k_weight, "k_weight", f32, (D,), device),
-                      self.eps, _need(self.inv_freq, "inv_freq", f32, (half,), device), 2 * half,
-                      1 if self.interleaved else 0, self.rot_scale)
+    _c: dict = field(default_factory=dict, repr=False, compare=False)
+
+    def struct(self, D: int, dev: int) -> _PrepC:
+        """The C structure for heads of D on GPU `dev`, built and checked once."""
+        c = self._c.get((D, dev))
+        if c is None:
+            f32 = torch.float32
+            half = 0 if self.inv_freq is None else self.inv_freq.numel()
+            c = self._c[(D, dev)] = _PrepC(
+                _need(self.q_weight, "q_weight", f32, (D,), dev), _need(self.k_weight, "k_weight", f32, (D,), dev), self.eps,
+                _need(self.inv_freq, "inv_freq", f32, (half,), dev), 2 * half, 1 if self.interleaved else 0, self.rot_scale)
+        return c
 
 
 def moe_qk_norm_rope(q, k, positions, prep: QKPrep, q_out, k_out, stream=None):
     """Norm and rotation of q [T][Hq][D] and k [T][Hkv][D] (either may be None) into contiguous
-    outputs; positions int32 [T]."""
+    outputs; positions int32 [T] (None without a rotation)."""
     x = q if q is not None else k
     if x is None or x.dim() != 3:
         raise ValueError("q or k must be given, as [T][heads][D]")
     T, _, D = x.shape
-    dev = x.device
-    qp, qs = (None, 0) if q is None else _head_rows(q, "q", T, D, dev)
-    kp, ks = (None, 0) if k is None else _head_rows(k, "k", T, D, dev)
-    Hq, Hkv = (0 if q is None else q.shape[1]), (0 if k is None else k.shape[1])
+    dev = x.get_device()
+    qp, qs, Hq = (None, 0, 0) if q is None else _head_rows(q, "q", T, D, dev)
+    kp, ks, Hkv = (None, 0, 0) if k is None else _head_rows(k, "k", T, D, dev)
     qo = None if q is None else _need(q_out, "q_out", q.dtype, (T, Hq, D), dev)
     ko = None if k is None else _need(k_out, "k_out", k.dtype, (T, Hkv, D), dev)
     pos = _need(positions, "positions", torch.int32, (T,), dev)
-    c = prep.struct(D, dev)
-    with _On(dev, stream) as s:
-        _check("moe_qk_norm_rope", lib().moe_qk_norm_rope(qp, qs, kp, ks, T, Hq, Hkv, D, pos, ctypes.byref(c), qo, ko, s))
+    _call("moe_qk_norm_rope", dev, stream, qp, qs, kp, ks, T, Hq, Hkv, D, pos, ctypes.byref(prep.struct(D, dev)), qo, ko)
 
 
 def nvfp4_kv_append(q, k, v, positions, slots, prep: QKPrep, cache: KVCache, q_out, stream=None):
@@ -487,21 +475,15 @@ def nvfp4_kv_append(q, k, v, positions, slots, prep: QKPrep, cache: KVCache, q_o
     (with q_out) may be None."""
     if k.dim() != 3:
         raise ValueError("k must be [T][Hkv][D]")
-    T, Hkv, D = k.shape
-    dev = cache.device
-    if (Hkv, D) != (cache.Hkv, cache.D) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [T][{cache.Hkv}][{cache.D}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    Hq = 0 if q is None else q.shape[1]
-    qp, qs = (None, 0) if q is None else _head_rows(q, "q", T, D, dev)
-    kp, ks = _head_rows(k, "k", T, D, dev)
-    vp, vs = _head_rows(v, "v", T, D, dev)
+    T, D, dev, i32 = k.shape[0], cache.D, cache.dev, torch.int32
+    if k.shape != (T, cache.Hkv, D) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [T][{cache.Hkv}][{D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    qp, qs, Hq = (None, 0, 0) if q is None else _head_rows(q, "q", T, D, dev)
+    kp, ks, _ = _head_rows(k, "k", T, D, dev)
+    vp, vs, _ = _head_rows(v, "v", T, D, dev)
     qo = None if q is None else _need(q_out, "q_out", q.dtype, (T, Hq, D), dev)
-    pos = _need(positions, "positions", torch.int32, (T,), dev)
-    sl = _need(slots, "slots", torch.int32, (T,), dev)
-    c = prep.struct(D, dev)
-    with _On(dev, stream) as s:
-        _check("nvfp4_kv_append", lib().nvfp4_kv_append(
-            qp, qs, kp, ks, vp, vs, T, Hq, pos, sl, ctypes.byref(c), ctypes.byref(cache._c), qo, s))
+    pos, sl = _need(positions, "positions", i32, (T,), dev), _need(slots, "slots", i32, (T,), dev)
+    _call("nvfp4_kv_append", dev, stream, qp, qs, kp, ks, vp, vs, T, Hq, pos, sl, ctypes.byref(prep.struct(D, dev)), cache.ref, qo)
 
 
 def nvfp4_kv_read(cache: KVCache, slots, k_out, v_out, stream=None):
@@ -510,15 +492,14 @@ def nvfp4_kv_read(cache: KVCache, slots, k_out, v_out, stream=None):
     out = k_out if k_out is not None else v_out
     if out is None:
         raise ValueError("k_out or v_out must be given")
-    n, dev = slots.numel(), cache.device
-    if out.dtype not in (torch.bfloat16, torch.int16, torch.float32):
+    n, dev = slots.numel(), cache.dev
+    f32 = out.dtype is torch.float32
+    if not f32 and out.dtype is not torch.bfloat16 and out.dtype is not torch.int16:
         raise ValueError("k_out and v_out must be bf16 or float32")
     shape = (n, cache.Hkv, cache.D)
     ko, vo = _need(k_out, "k_out", out.dtype, shape, dev), _need(v_out, "v_out", out.dtype, shape, dev)
     sl = _need(slots, "slots", torch.int32, (n,), dev)
-    with _On(dev, stream) as s:
-        _check("nvfp4_kv_read", lib().nvfp4_kv_read(
-            ctypes.byref(cache._c), sl, n, MOE_TYPE_F32 if out.dtype is torch.float32 else MOE_TYPE_BF16, ko, vo, s))
+    _call("nvfp4_kv_read", dev, stream, cache.ref, sl, n, MOE_TYPE_F32 if f32 else MOE_TYPE_BF16, ko, vo)
 
 
 def nvfp4_kv_attention_workspace(T: int, n_seqs: int, max_q: int, Hq: int, cache: KVCache) -> int:
@@ -536,15 +517,13 @@ def nvfp4_kv_attention(q, cu_q, ctx_lens, block_table, max_q: int, cache: KVCach
     T, Hq, D = q.shape
     if D != cache.D:
         raise ValueError(f"q has heads of {D}, the cache of {cache.D}")
-    dev, i32 = cache.device, torch.int32
+    dev, i32 = cache.dev, torch.int32
     n, pages = block_table.shape
-    qp, qs = _head_rows(q, "q", T, D, dev)
+    qp, qs, _ = _head_rows(q, "q", T, D, dev)
     cu, ctx = _need(cu_q, "cu_q", i32, (n + 1,), dev), _need(ctx_lens, "ctx_lens", i32, (n,), dev)
     table = _need(block_table, "block_table", i32, (n, pages), dev)
     o, e = _need(out, "out", q.dtype, (T, Hq, D), dev), _need(lse, "lse", torch.float32, (T, Hq), dev)
-    if ws is None or ws.device != dev:
-        raise ValueError(f"ws must be on {dev}")
-    with _On(dev, stream) as s:
-        _check("nvfp4_kv_attention", lib().nvfp4_kv_attention(
-            qp, qs, T, Hq, cu, ctx, table, n, pages, max_q, ctypes.byref(cache._c), scale, 1 if causal else 0, o, e,
-            _ptr(ws), ws.numel() * ws.element_size(), s))
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on device {dev}")
+    _call("nvfp4_kv_attention", dev, stream, qp, qs, T, Hq, cu, ctx, table, n, pages, max_q, cache.ref, scale,
+          1 if causal else 0, o, e, ws.data_ptr(), ws.numel() * ws.element_size())
