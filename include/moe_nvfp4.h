@@ -400,9 +400,9 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   Rows of a page number outside [0, n_pages) count as zeros, and set the device status to
  *   MOE_ERR_INVALID_ARG; cu_q (ascending) is read as clamped to [0, T] and ctx_lens to the table.
  *   The sums, maxima and outputs are float32, the softmax weights rounded to float16 and the
- *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes; it needs no
- *   initialisation, and calls that may overlap need one each. Results do not depend on what
- *   runs beside the call.
+ *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes, which need no
+ *   initialisation and may serve calls of any sizes up to those, one after the other; calls that
+ *   may overlap need one each. The same call gives the same bits every time.
  * Limits: D and page_size as the cache, Hq <= 1024, n_seqs <= 65536, T * Hq < 2^31.
  */
 moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq, const int32_t* cu_q,

@@ -177,7 +177,7 @@ void set_prep(QkvPrepArgs* a, const moe_qk_prep_t& p, const int32_t* positions) 
 // kernel (where some sequence can have that many rows), and the partial results of the kernel
 // that runs (the two run one after the other).
 struct KvAttnWs {
-  size_t meta, tiles, partial, part_stride, bytes;
+  size_t meta, tiles, partial, bytes;
   bool tc;
 };
 KvAttnWs kv_attn_ws(int sms, int64_t T, int n_seqs, int64_t max_q, int G, int D) {

@@ -240,6 +240,7 @@ int kv_attn_tc_max_tiles(int64_t T, int n_seqs, int G);
 size_t kv_attn_tc_tiles_bytes(int64_t T, int n_seqs, int G);
 cudaError_t init_kv_attn_tc_attributes();
 cudaError_t set_wait_limit_kv_attn_tc(unsigned long long ns);
+cudaError_t set_wait_limit_kv_attn_dec(unsigned long long ns);
 cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st);
 cudaError_t init_kv_attn_dec_attributes();
 cudaError_t launch_kv_attn_dec(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st);
@@ -254,6 +255,7 @@ inline cudaError_t set_wait_limits(unsigned long long ns) {
   cudaError_t e = set_wait_limit_ffn_decode(ns);
   if (e == cudaSuccess) e = set_wait_limit_router_tc(ns);
   if (e == cudaSuccess) e = set_wait_limit_kv_attn_tc(ns);
+  if (e == cudaSuccess) e = set_wait_limit_kv_attn_dec(ns);
   if (e == cudaSuccess) e = set_wait_limit_ffn_tc(ns);
   if (e == cudaSuccess) e = set_wait_limit_ffn_dec(ns);
   if (e == cudaSuccess) e = set_wait_limit_layer_dec(ns);

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace moe {
 
@@ -38,6 +39,27 @@ MOE_DEV uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// mbar_wait with the limit read once per block: short in code (the roles of a block share the
+// instruction caches) and without a load from global memory in every wait.
+struct Patience {
+  volatile int abort;
+  unsigned long long limit;
+};
+MOE_DEV bool wait_soon(uint64_t* bar, uint32_t parity, Patience* w, int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (w->abort) return false;
+    if (globaltimer_ns() - t0 > w->limit) {
+      w->abort = 1;
+      atomicExch(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 
 // A sequence of the batch, clamped so that no index made from it leaves its array.

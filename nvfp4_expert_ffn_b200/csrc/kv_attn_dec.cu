@@ -2,37 +2,63 @@
 // speculative tokens): out = softmax(scale q K^T) V with K and V read as 4-bit codes.
 //
 // Bound by the cache's bytes: 9/16 byte per element of K and V, read once per group of 8 NR
-// query rows. A byte of codes is two elements, so the work per byte is what has to be small:
-// the codes go from global memory straight into the operand registers of mma.sync (m16n8k16,
-// float16 in, float32 out) without passing shared memory. The tensor pipe is idle most of the
-// time here (8 query columns), tcgen05 would need the expanded tiles in shared memory.
+// query rows. A byte of codes is two elements, so the instructions per byte are what has to be
+// few: the codes come by bulk copies into a ring that each warp keeps for itself (32 keys a
+// stage, no registers and no address arithmetic while they are under way) and go from there
+// straight into the operand registers of mma.sync (m16n8k16, float16 in, float32 out). The
+// tensor pipe is idle most of the time here (8 query columns); tcgen05 would need the expanded
+// tiles in shared memory.
 //   S^T = K Q^T: keys are the 16 rows of the A operand. The order of the head's elements
 //     along k is free as long as K and Q agree, so a thread's share of a key row is one
 //     contiguous quarter: 16-byte loads, and a byte of codes expands (one conversion) to one
 //     f16x2 register of the fragment, times the block's scale (one multiply, exact: 2 + 4
 //     significant bits).
 //   O^T = V^T P^T: the A operand pairs two keys of one element, so the codes of two keys are
-//     interleaved nibble by nibble first (half an instruction per element); the scores'
-//     fragments turn into P^T operands with movmatrix.
+//     interleaved nibble by nibble first (a quarter of an instruction per element); the scores'
+//     fragments turn into P^T operands with movmatrix. Row r of a tile is key key_of(r), which
+//     makes a thread's four keys of V four rows apart: a warp reads four whole rows at a time.
 // q is scaled by a power of two per row into float16's range (exact; the factor returns in
 // the softmax scale), the weights P are rounded to float16 (11 bits; the result is bf16, 8),
 // sums, maxima and the output stay in float32.
 //
 // The keys of all sequences and heads are cut into chunks of kChunk and dealt to the blocks in
-// equal contiguous runs, so a batch of any shape fills the machine; a run that starts or ends
+// equal contiguous runs, so a batch of any shape fills the machine. A run that starts or ends
 // inside a sequence leaves its partial result (row maxima, sums, unnormalised output) in the
-// workspace, and a second small kernel joins them in a fixed order.
+// workspace, and a second small kernel joins them, a block a row, in the order of the keys. (The
+// last block to finish a sequence joining its parts itself took longer: 14 us for nine parts of a
+// D = 256 head, one load latency after another in a single block, against 3 us.)
 #include <cuda_bf16.h>
 
 #include "kv_attn.cuh"
+#include "sm100.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kDecWarps = 8;
-constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kChunk = 64;  // keys
+constexpr int kChunk = 64;       // keys of a unit of work
+constexpr int kStageKeys = 32;   // keys of a warp's stage
+constexpr int kStages = 2;
+
+// Warps of a block: what the registers of an SM allow (O and Q alone are 12 D / 32 NR of them).
+__host__ __device__ constexpr int dec_warps(int D, int NR) { return D == 256 && NR == 1 ? 12 : 8; }
+__host__ __device__ constexpr int dec_blocks(int D, int NR) { return D == 256 || NR > 1 ? 1 : 2; }  // of an SM
+__host__ __device__ constexpr int stage_bytes(int D) { return kStageKeys * 2 * (D / 2 + D / 16); }
+// The warps' outputs side by side: rows of D + 8 floats, so that the two rows' stores of lanes
+// 8 apart fall into different banks. They lie over the ring where there is no room beside it.
+__host__ __device__ constexpr int join_bytes(int D, int NR) { return dec_warps(D, NR) * 8 * NR * (D + 8) * 4; }
+__host__ __device__ constexpr int ring_bytes(int D, int NR) { return dec_warps(D, NR) * kStages * stage_bytes(D); }
+__host__ __device__ constexpr bool join_apart(int D, int NR) {
+  return (ring_bytes(D, NR) + join_bytes(D, NR) + 2048) * dec_blocks(D, NR) <= 226 * 1024;
+}
+__host__ __device__ constexpr int dec_smem(int D, int NR) {
+  const int ring = ring_bytes(D, NR), join = join_bytes(D, NR);
+  return join_apart(D, NR) ? ring + join : ring > join ? ring : join;
+}
+
+// the key of a tile's row r: the rows that one thread holds as the k index of V (2c, 2c + 1,
+// 2c + 8, 2c + 9) are keys c, c + 4, c + 8, c + 12
+MOE_DEV int key_of(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
 
 MOE_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -48,18 +74,18 @@ MOE_DEV uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-template <int BYTES>
-MOE_DEV void load_codes(uint32_t* dst, const uint8_t* src) {
-  if constexpr (BYTES == 4) {
-    dst[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-  } else if constexpr (BYTES == 8) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+template <int WORDS>
+MOE_DEV void load_words(uint32_t* dst, const uint8_t* src) {
+  if constexpr (WORDS == 1) {
+    dst[0] = *reinterpret_cast<const uint32_t*>(src);
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
     dst[0] = v.x;
     dst[1] = v.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[i];
       dst[4 * i] = v.x;
       dst[4 * i + 1] = v.y;
       dst[4 * i + 2] = v.z;
@@ -70,49 +96,10 @@ MOE_DEV void load_codes(uint32_t* dst, const uint8_t* src) {
 
 template <int BYTES>
 MOE_DEV uint32_t load_scales(const uint8_t* src) {
-  if constexpr (BYTES == 1) return __ldg(src);
-  if constexpr (BYTES == 2) return __ldg(reinterpret_cast<const uint16_t*>(src));
-  return __ldg(reinterpret_cast<const uint32_t*>(src));
+  if constexpr (BYTES == 1) return *src;
+  if constexpr (BYTES == 2) return *reinterpret_cast<const uint16_t*>(src);
+  return *reinterpret_cast<const uint32_t*>(src);
 }
-
-// One thread's share of 16 keys: of K, rows g and g + 8, a quarter c of the head each; of V,
-// keys 2c, 2c+1, 2c+8, 2c+9, an eighth g of the head each.
-template <int D>
-struct Tile {
-  static constexpr int KW = D / 32, VW = D / 64;  // words of codes per row
-  static constexpr int KS = D / 64;               // scale bytes per K row
-  static constexpr int VS = D >= 128 ? D / 128 : 1;
-  uint32_t k[2][KW], v[4][VW];
-  uint32_t ks[2], vs[4];
-
-  MOE_DEV void zero() {  // rows of a page number outside the cache
-#pragma unroll
-    for (int i = 0; i < KW; ++i) k[0][i] = k[1][i] = 0u;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) v[0][i] = v[1][i] = v[2][i] = v[3][i] = 0u;
-    ks[0] = ks[1] = vs[0] = vs[1] = vs[2] = vs[3] = 0u;
-  }
-
-  MOE_DEV void load(const KvCacheArgs& c, int64_t row0, int g, int q) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t row = row0 + g + 8 * i;
-      load_codes<KW * 4>(k[i], c.k_codes + row * (D / 2) + q * (D / 8));
-      ks[i] = load_scales<KS>(c.k_scales + row * (D / 16) + q * KS);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = row0 + 2 * q + (i & 1) + 8 * (i >> 1);
-      load_codes<VW * 4>(v[i], c.v_codes + row * (D / 2) + g * (D / 16));
-      vs[i] = load_scales<VS>(c.v_scales + row * (D / 16) + (D >= 128 ? g * VS : g / 2));
-    }
-  }
-};
-
-struct Segment {
-  int b, h, rg;      // sequence, key head, group of rows
-  int k0, k1, n_ch;  // chunks [k0, k1) of the item's n_ch
-};
 
 MOE_DEV int seq_chunks(const SeqSpan& s) { return max(1, (s.ctx + kChunk - 1) / kChunk); }
 
@@ -123,25 +110,66 @@ MOE_DEV int64_t seq_cost(const KvAttnArgs& a, const SeqSpan& s, int rows_per_gro
   return (int64_t)seq_chunks(s) * a.cache.Hkv * ((rows + rows_per_group - 1) / rows_per_group);
 }
 
+// Rows of outputs are kept in the order of the fragments: place 16 i + 2 g + e holds element
+// g D / 8 + 2 i + e (m tile i, thread row g). Writes the four places from 4 q on.
+template <int D>
+MOE_DEV void write_row(const KvAttnArgs& a, const SeqSpan& sq, int h, int rr, int q, float4 v, float mm, float ll, float vts) {
+  const int tok = rr / a.G;
+  const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + h * a.G + rr - tok * a.G;
+  const float f = ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
+  uint16_t* dst = a.out + out_row * D + (q & 3) * 2 * (D / 8) + (q >> 2) * 2;
+  *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(v.x * f, v.y * f);
+  *reinterpret_cast<__nv_bfloat162*>(dst + D / 8) = __floats2bfloat162_rn(v.z * f, v.w * f);
+  if (a.lse && q == 0) a.lse[out_row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+}
+
+// A run of key chunks [k0, k1) of one sequence, key head and group of rows.
+struct Item {
+  SeqSpan sq;
+  int b, h, row_first, k0, k1, n_ch;
+  long long at;  // its end, counted in chunks over all items
+};
+
 template <int D, int NR>
-__global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_attn_dec_kernel(const KvAttnArgs a) {
-  constexpr int RB = 8 * NR;
+__global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_attn_dec_kernel(const KvAttnArgs a) {
+  constexpr int RB = 8 * NR, W = dec_warps(D, NR), THREADS = 32 * W;
   constexpr int KSTEPS = D / 16;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  float* s_o = reinterpret_cast<float*>(smem_raw);  // [warps][RB][D]
-  __shared__ float s_m[kDecWarps][RB], s_l[kDecWarps][RB], s_f[kDecWarps][RB];
+  constexpr int KW = D / 32, VW = D / 64;  // words of codes that a thread holds of a K row, of a V row
+  constexpr int KS = D / 64, VS = D >= 128 ? D / 128 : 1;  // bytes of scales
+  // a stage: codes of K, codes of V, scales of K, scales of V
+  constexpr int kV = kStageKeys * D / 2, kKs = 2 * kV, kVs = kKs + kStageKeys * D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr bool kApart = join_apart(D, NR);
+  float* s_o = reinterpret_cast<float*>(smem + (kApart ? ring_bytes(D, NR) : 0));  // [warps][RB][D + 8]
+  __shared__ uint64_t s_full[W][kStages];
+  __shared__ uint32_t s_bad[W][kStages];  // 16-key halves whose page number is outside the cache
+  __shared__ float s_m[W][RB], s_l[W][RB];
   __shared__ float s_mm[RB], s_ll[RB];
-  __shared__ long long s_scan[kDecWarps];
-  __shared__ int s_b;
+  __shared__ long long s_scan[W];
   __shared__ long long s_local;
-  MOE_PDL_PROLOGUE();
+  __shared__ SeqSpan s_seq;
+  __shared__ int s_b;
+  __shared__ Patience s_wait;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  if (tid < W * kStages) {
+    mbar_init(&s_full[tid / kStages][tid % kStages], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    s_wait.abort = 0;
+    s_wait.limit = wait_limit_ns();
+  }
+  MOE_PDL_PROLOGUE();
 
   // ---- this block's run of chunks
-  const int per = (a.n_seqs + kDecThreads - 1) / kDecThreads;
+  const int per = (a.n_seqs + THREADS - 1) / THREADS;
   const int b_lo = min(tid * per, a.n_seqs), b_hi = min(b_lo + per, a.n_seqs);
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_cost(a, load_seq(a, b), RB);
+  SeqSpan one = {};  // of a thread with one sequence, read once
+  for (int b = b_lo; b < b_hi; ++b) {
+    one = load_seq(a, b);
+    mine += seq_cost(a, one, RB);
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -151,7 +179,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
   long long before = 0, total = 0;
-  for (int w = 0; w < kDecWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
@@ -163,8 +191,10 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
   if (mine > 0 && before <= c_begin && c_begin < before + mine) {
     long long at = before;
     for (int b = b_lo; b < b_hi; ++b) {
-      const long long cost = seq_cost(a, load_seq(a, b), RB);
+      const SeqSpan sq = per == 1 ? one : load_seq(a, b);
+      const long long cost = seq_cost(a, sq, RB);
       if (c_begin < at + cost) {
+        s_seq = sq;
         s_b = b;
         s_local = c_begin - at;
         break;
@@ -174,49 +204,107 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
   }
   __syncthreads();
 
-  long long left = c_end - c_begin;
-  int b = s_b;
-  long long local = s_local;
-  long long at = c_begin;  // global index of the next chunk
-  while (left > 0 && b < a.n_seqs) {
-    const SeqSpan sq = load_seq(a, b);
-    const long long cost = seq_cost(a, sq, RB);
-    if (local >= cost) {
-      local = 0;
-      ++b;
-      continue;
-    }
-    const int n_ch = seq_chunks(sq);
-    const int rows = sq.n_q * a.G, n_rg = (rows + RB - 1) / RB;
-    const int item = (int)(local / n_ch), k0 = (int)(local - (long long)item * n_ch);
-    const int k1 = (int)min((long long)n_ch, k0 + left);
-    const int h = item / n_rg, rg = item - h * n_rg;
-    const int row_first = rg * RB;
-    local += k1 - k0;
-    left -= k1 - k0;
-    at += k1 - k0;
+  uint8_t* ring = smem + warp * kStages * stage_bytes(D);
+  uint32_t n_issued = 0, n_used = 0;  // this warp's stages
+  const int ps = a.cache.page_size, rows_copy = min(ps, kStageKeys), copies = kStageKeys / rows_copy;
+  // lanes 0..7 copy: array lane / 2 (codes of K, of V, scales of K, of V), part lane % 2
+  const int arr = lane >> 1, part = lane & 1;
+  const uint8_t* arr_src = arr == 0 ? a.cache.k_codes : arr == 1 ? a.cache.v_codes : arr == 2 ? a.cache.k_scales : a.cache.v_scales;
+  const int arr_row = arr < 2 ? D / 2 : D / 16;
+  const int arr_at = (arr == 0 ? 0 : arr == 1 ? kV : arr == 2 ? kKs : kVs) + part * rows_copy * arr_row;
 
+  // ---- the runs of this block, one after the other
+  long long at = c_begin, local = s_local;
+  int b = s_b;
+  SeqSpan sq = s_seq;
+  auto next_item = [&](Item* it) {
+    while (at < c_end && b < a.n_seqs) {
+      const long long cost = seq_cost(a, sq, RB);
+      if (local < cost) {
+        const int n_ch = seq_chunks(sq), n_rg = (sq.n_q * a.G + RB - 1) / RB;
+        const int item = (int)(local / n_ch), k0 = (int)(local - (long long)item * n_ch);
+        const int k1 = (int)min((long long)n_ch, k0 + c_end - at);
+        local += k1 - k0;
+        at += k1 - k0;
+        *it = Item{sq, b, item / n_rg, item % n_rg * RB, k0, k1, n_ch, at};
+        return true;
+      }
+      local = 0;
+      if (++b < a.n_seqs) sq = load_seq(a, b);
+    }
+    return false;
+  };
+
+  // ---- keys: stages of 32, dealt to the warps in turn
+  constexpr int kStep = W * kStageKeys;
+  int t_issue = 0, page = -2;
+  auto tok_end_of = [](const Item& it) { return min(it.k1 * kChunk, it.sq.ctx); };
+  auto page_of = [&](const Item& it, int t) {  // of this lane's copy of the stage that starts at key t; read a stage early
+    t += part * rows_copy;
+    return lane < 8 && part < copies && t < tok_end_of(it)
+               ? __ldg(a.block_table + (int64_t)it.b * a.max_pages + (t >> a.page_shift))
+               : -2;
+  };
+  auto issue = [&](const Item& it) {
+    const int next = page_of(it, t_issue + kStep);
+    if (t_issue < tok_end_of(it)) {
+      const uint32_t slot = n_issued++ % kStages;
+      const bool good = page >= 0 && page < a.cache.n_pages;
+      const uint32_t bads = __ballot_sync(0xffffffffu, page != -2 && !good), goods = __ballot_sync(0xffffffffu, good);
+      if (lane == 0) {
+        if (bads) atomicExch(a.status, kStatusInvalid);
+        s_bad[warp][slot] = copies == 1 ? (bads ? 3u : 0u) : bads & 3u;
+        mbar_arrive_expect_tx(&s_full[warp][slot], (__popc(goods & 0x0Fu) * (D / 2) + __popc(goods & 0xF0u) * (D / 16)) * rows_copy);
+      }
+      __syncwarp();
+      if (good) {
+        const int64_t row = ((int64_t)page * a.cache.Hkv + it.h) * ps + ((t_issue + part * rows_copy) & (ps - 1));
+        bulk_g2s(ring + slot * stage_bytes(D) + arr_at, arr_src + row * arr_row, rows_copy * arr_row, &s_full[warp][slot]);
+      }
+    }
+    page = next;
+    t_issue += kStep;
+  };
+  auto prime = [&](const Item& it) {
+    t_issue = it.k0 * kChunk + warp * kStageKeys;
+    page = page_of(it, t_issue);
+  };
+  auto fill = [&](const Item& it) {
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) issue(it);
+  };
+
+  Item it, coming;
+  bool more = next_item(&it), filled = false;
+  while (more) {
+    if (!filled) prime(it);  // (the page number comes beside the queries)
+    const int tok_end = tok_end_of(it), rows = it.sq.n_q * a.G, row_first = it.row_first, h = it.h;
     // ---- queries: thread (g, c) holds row g's quarter c as the B operand of every k step
+    uint4 raw[NR][D / 32];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = row_first + 8 * r + g;
+      const bool ok = row < rows;
+      const int tok = ok ? row / a.G : 0, head = h * a.G + (ok ? row - tok * a.G : 0);
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(it.sq.q0 + tok) * a.q_stride + (int64_t)head * D +
+                                                        c * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw[r][i] = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (!filled) fill(it);
     uint32_t bq[NR][KSTEPS][2];
     float fac[NR][2];
     int lim[NR][2], lim_min = 0x7fffffff;
     const float kts = a.cache.k_ts ? a.cache.k_ts[h] : 1.0f;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int row = row_first + 8 * r + g;
-      const bool ok = row < rows;
-      const int tok = ok ? row / a.G : 0, head = h * a.G + (ok ? row - tok * a.G : 0);
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride + (int64_t)head * D +
-                                                        c * (D / 4));
-      uint4 raw[D / 32];
       uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        raw[i] = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, raw[i].w & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[r][i].x & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[r][i].y & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[r][i].z & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[r][i].w & 0x7FFF7FFFu);
       }
       int e = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
@@ -225,7 +313,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
       const float up = __int_as_float((127 + 13 - e) << 23);  // the row's largest element becomes 2^13..2^14
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const uint32_t w[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           bq[r][2 * i + (j >> 1)][j & 1] =
@@ -237,7 +325,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
         fac[r][j] = a.scale * kLog2e * kts * __int_as_float((127 - 13 + ej) << 23);
         const int rj = row_first + 8 * r + 2 * c + j;
         // keys that row may see: all of the context, or up to its own position
-        lim[r][j] = rj >= rows ? 0 : a.causal ? max(sq.ctx - sq.n_q + rj / a.G + 1, 0) : sq.ctx;
+        lim[r][j] = rj >= rows ? 0 : a.causal ? max(it.sq.ctx - it.sq.n_q + rj / a.G + 1, 0) : it.sq.ctx;
         if (rj < rows) lim_min = min(lim_min, lim[r][j]);
       }
     }
@@ -256,137 +344,140 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
       l[r][0] = l[r][1] = 0.0f;
     }
 
-    // ---- keys: tiles of 16, dealt to the warps in turn
-    const int tok_end = min(k1 * kChunk, sq.ctx);
-    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-    const int ps = a.cache.page_size, psl = a.page_shift;
-    auto page_of = [&](int t0) -> int {
-      if (t0 >= tok_end) return -1;
-      const int page = __ldg(table + (t0 >> psl));
-      if (page < 0 || page >= a.cache.n_pages) {
-        if (lane == 0) atomicExch(a.status, kStatusInvalid);
-        return -1;
-      }
-      return page;
-    };
-    auto row_of = [&](int page, int t0) -> int64_t {
-      return ((int64_t)page * a.cache.Hkv + h) * ps + (t0 & (ps - 1));
-    };
-    int t0 = k0 * kChunk + warp * 16;
-    const int page = page_of(t0);
-    Tile<D> cur, nxt;
-    if (page >= 0)
-      cur.load(a.cache, row_of(page, t0), g, c);
-    else
-      cur.zero();
-    int page_n = page_of(t0 + kDecWarps * 16);
-    for (; t0 < tok_end; t0 += kDecWarps * 16) {
-      const int t1 = t0 + kDecWarps * 16;
-      if (page_n >= 0)
-        nxt.load(a.cache, row_of(page_n, t1), g, c);
-      else
-        nxt.zero();
-      const int page_nn = page_of(t1 + kDecWarps * 16);
-      // S^T = K Q^T
-      float s[NR][4];
+#pragma unroll 1
+    for (int t_stage = it.k0 * kChunk + warp * kStageKeys; t_stage < tok_end; t_stage += kStep) {
+      const uint32_t slot = n_used % kStages;
+      if (!__all_sync(0xffffffffu, wait_soon(&s_full[warp][slot], (n_used / kStages) & 1, &s_wait, a.status))) break;
+      ++n_used;
+      const uint8_t* st = ring + slot * stage_bytes(D);
+      const uint32_t bad = s_bad[warp][slot];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
+      for (int half = 0; half < 2; ++half) {
+        const int t0 = t_stage + 16 * half;
+        if (t0 >= tok_end) break;
+        const uint8_t* kc = st + (16 * half + key_of(g)) * (D / 2) + c * (D / 8);
+        const uint8_t* vc = st + kV + (16 * half + c) * (D / 2) + g * (D / 16);
+        uint32_t kk[2][KW], vv[4][VW], ks[2], vs[4];
 #pragma unroll
-      for (int w = 0; w < Tile<D>::KW; ++w) {  // 8 elements of both rows: two k steps
-        uint32_t f0[4], f1[4];
-        e2m1x8_to_f16x2x4(cur.k[0][w], f0);
-        e2m1x8_to_f16x2x4(cur.k[1][w], f1);
-        // the scale of block w / 2 of this quarter in both halves
-        const uint32_t sel = (w / 2) * 0x0011u;
-        const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(cur.ks[0], 0, sel)),
-                       s1 = e4m3x2_to_f16x2(__byte_perm(cur.ks[1], 0, sel));
+        for (int i = 0; i < 2; ++i) {
+          load_words<KW>(kk[i], kc + i * 8 * (D / 2));
+          ks[i] = load_scales<KS>(st + kKs + (16 * half + key_of(g) + 8 * i) * (D / 16) + c * KS);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          f0[i] = hmul2(f0[i], s0);
-          f1[i] = hmul2(f1[i], s1);
+          load_words<VW>(vv[i], vc + i * 4 * (D / 2));
+          vs[i] = load_scales<VS>(st + kVs + (16 * half + c + 4 * i) * (D / 16) + (D >= 128 ? g * VS : g / 2));
         }
+        if ((bad >> half) & 1u) ks[0] = ks[1] = vs[0] = vs[1] = vs[2] = vs[3] = 0u;  // rows of no page count as zeros
+        // S^T = K Q^T
+        float s[NR][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t fa[4] = {f0[2 * u], f1[2 * u], f0[2 * u + 1], f1[2 * u + 1]};
+        for (int r = 0; r < NR; ++r) s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
 #pragma unroll
-          for (int r = 0; r < NR; ++r) mma_f16(s[r], fa, bq[r][2 * w + u][0], bq[r][2 * w + u][1]);
+        for (int w = 0; w < KW; ++w) {  // 8 elements of both rows: two k steps
+          uint32_t f0[4], f1[4];
+          e2m1x8_to_f16x2x4(kk[0][w], f0);
+          e2m1x8_to_f16x2x4(kk[1][w], f1);
+          // the scale of block w / 2 of this quarter in both halves
+          const uint32_t sel = (w / 2) * 0x0011u;
+          const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(ks[0], 0, sel)), s1 = e4m3x2_to_f16x2(__byte_perm(ks[1], 0, sel));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t fa[4] = {hmul2(f0[2 * u], s0), hmul2(f1[2 * u], s1), hmul2(f0[2 * u + 1], s0), hmul2(f1[2 * u + 1], s1)};
+#pragma unroll
+            for (int r = 0; r < NR; ++r) mma_f16(s[r], fa, bq[r][2 * w + u][0], bq[r][2 * w + u][1]);
+          }
         }
-      }
-      // softmax: columns (query rows) 2c and 2c + 1, keys g and g + 8
-      const bool edge = t0 + 16 > lim_min;
-      uint32_t pb[NR][2];
-      bool raise = false;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[r][j] *= fac[r][j & 1];
-          if (edge && t0 + g + 8 * (j >> 1) >= lim[r][j & 1]) s[r][j] = -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) raise |= fmaxf(s[r][j], s[r][j + 2]) > m[r][j] + kRaise;
-      }
-      if (__any_sync(0xffffffffu, raise)) {
+        // softmax: columns (query rows) 2c and 2c + 1, tile rows g and g + 8
+        const bool edge = t0 + 16 > lim_min;
+        uint32_t pb[NR][2];
+        bool raise = false;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float fix[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float x = fmaxf(s[r][j], s[r][j + 2]);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            x = fmaxf(x, m[r][j]);
-            fix[j] = ex2(m[r][j] - x);
-            m[r][j] = x;
-            l[r][j] *= fix[j];
+          for (int j = 0; j < 4; ++j) {
+            s[r][j] *= fac[r][j & 1];
+            if (edge && t0 + key_of(g) + 8 * (j >> 1) >= lim[r][j & 1]) s[r][j] = -INFINITY;
           }
 #pragma unroll
-          for (int i = 0; i < KSTEPS; ++i)
+          for (int j = 0; j < 2; ++j) raise |= fmaxf(s[r][j], s[r][j + 2]) > m[r][j] + kRaise;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[r][i][j] *= fix[j & 1];
+          for (int r = 0; r < NR; ++r) {
+            float fix[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float x = fmaxf(s[r][j], s[r][j + 2]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+              x = fmaxf(x, m[r][j]);
+              fix[j] = ex2(m[r][j] - x);
+              m[r][j] = x;
+              l[r][j] *= fix[j];
+            }
+#pragma unroll
+            for (int i = 0; i < KSTEPS; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[r][i][j] *= fix[j & 1];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          float p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = ex2(s[r][j] - m[r][j & 1]);
+          l[r][0] += p[0] + p[2];
+          l[r][1] += p[1] + p[3];
+          pb[r][0] = transpose8x8(pack_f16(p[0], p[1]));
+          pb[r][1] = transpose8x8(pack_f16(p[2], p[3]));
+        }
+        // O^T += V^T P^T
+        if (t0 + 16 > it.sq.ctx) {  // keys past the end: whatever the page holds there counts as 0
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t0 + c + 4 * i >= it.sq.ctx) vs[i] = 0;
+        }
+        const uint32_t va = __byte_perm(vs[0], vs[1], 0x5140), vb = __byte_perm(vs[2], vs[3], 0x5140);
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t sa = e4m3x2_to_f16x2(w < 2 ? va & 0xFFFFu : va >> 16),
+                         sb = e4m3x2_to_f16x2(w < 2 ? vb & 0xFFFFu : vb >> 16);
+          const uint32_t x0 = vv[0][w], x1 = vv[1][w], x2 = vv[2][w], x3 = vv[3][w];
+          constexpr uint32_t lo = 0x0F0F0F0Fu;
+          uint32_t fe[4], fo[4], he[4], ho[4];
+          e2m1x8_to_f16x2x4((x0 & lo) | ((x1 << 4) & ~lo), fe);
+          e2m1x8_to_f16x2x4(((x0 >> 4) & lo) | (x1 & ~lo), fo);
+          e2m1x8_to_f16x2x4((x2 & lo) | ((x3 << 4) & ~lo), he);
+          e2m1x8_to_f16x2x4(((x2 >> 4) & lo) | (x3 & ~lo), ho);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t fa[4] = {hmul2(fe[i], sa), hmul2(fo[i], sa), hmul2(he[i], sb), hmul2(ho[i], sb)};
+#pragma unroll
+            for (int r = 0; r < NR; ++r) mma_f16(o[r][4 * w + i], fa, pb[r][0], pb[r][1]);
+          }
         }
       }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = ex2(s[r][j] - m[r][j & 1]);
-        l[r][0] += p[0] + p[2];
-        l[r][1] += p[1] + p[3];
-        pb[r][0] = transpose8x8(pack_f16(p[0], p[1]));
-        pb[r][1] = transpose8x8(pack_f16(p[2], p[3]));
-      }
-      // O^T += V^T P^T
-      uint32_t vs[4] = {cur.vs[0], cur.vs[1], cur.vs[2], cur.vs[3]};
-      if (t0 + 16 > sq.ctx) {  // keys past the end: whatever the page holds there counts as 0
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t0 + 2 * c + (i & 1) + 8 * (i >> 1) >= sq.ctx) vs[i] = 0;
-      }
-      const uint32_t va = __byte_perm(vs[0], vs[1], 0x5140), vb = __byte_perm(vs[2], vs[3], 0x5140);
-#pragma unroll
-      for (int w = 0; w < Tile<D>::VW; ++w) {
-        const uint32_t sa = e4m3x2_to_f16x2(w < 2 ? va & 0xFFFFu : va >> 16),
-                       sb = e4m3x2_to_f16x2(w < 2 ? vb & 0xFFFFu : vb >> 16);
-        const uint32_t x0 = cur.v[0][w], x1 = cur.v[1][w], x2 = cur.v[2][w], x3 = cur.v[3][w];
-        constexpr uint32_t lo = 0x0F0F0F0Fu;
-        uint32_t fe[4], fo[4], he[4], ho[4];
-        e2m1x8_to_f16x2x4((x0 & lo) | ((x1 << 4) & ~lo), fe);
-        e2m1x8_to_f16x2x4(((x0 >> 4) & lo) | (x1 & ~lo), fo);
-        e2m1x8_to_f16x2x4((x2 & lo) | ((x3 << 4) & ~lo), he);
-        e2m1x8_to_f16x2x4(((x2 >> 4) & lo) | (x3 & ~lo), ho);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t fa[4] = {hmul2(fe[i], sa), hmul2(fo[i], sa), hmul2(he[i], sb), hmul2(ho[i], sb)};
-#pragma unroll
-          for (int r = 0; r < NR; ++r) mma_f16(o[r][4 * w + i], fa, pb[r][0], pb[r][1]);
-        }
-      }
-      cur = nxt;
-      page_n = page_nn;
+      __syncwarp();  // the stage has been read by all lanes
+      issue(it);
+    }
+    // (a wait that ran out: no copy may land in what follows)
+    for (; n_used < n_issued; ++n_used) {
+      volatile int no_abort = 0;
+      mbar_wait(&s_full[warp][n_used % kStages], (n_used / kStages) & 1, &no_abort, a.status);
     }
 
-    // ---- join the warps
+    // the next run's first keys come while this one is joined
+    more = next_item(&coming);
+    filled = kApart && more;
+    if (filled) {
+      prime(coming);
+      fill(coming);
+    }
+
+    // ---- join the warps' results
+    const bool whole = it.k0 == 0 && it.k1 == it.n_ch;
+    const float vts = a.cache.v_ts ? a.cache.v_ts[h] : 1.0f;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -399,118 +490,119 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 || NR > 1 ? 1 : 2) kv_at
         }
       }
     __syncthreads();
-    if (tid < RB) {
-      float mm = kNoMax, ll = 0.0f;
-      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, s_m[w][tid]);
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float f = ex2(s_m[w][tid] - mm);
-        s_f[w][tid] = f;
-        ll += s_l[w][tid] * f;
-      }
-      s_mm[tid] = mm;
-      s_ll[tid] = ll;
-    }
-    __syncthreads();
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = 8 * r + 2 * c + j;
-        const float f = s_f[warp][row];
-        float* dst = s_o + ((size_t)warp * RB + row) * D + g * (D / 8);
+        float mm = kNoMax;
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w][row]);
+        const float f = ex2(m[r][j] - mm);
+        float* dst = s_o + (warp * RB + row) * (D + 8) + 2 * g;
 #pragma unroll
         for (int i = 0; i < KSTEPS; ++i)
-          *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[r][i][j] * f, o[r][i][j + 2] * f);
+          *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[r][i][j] * f, o[r][i][j + 2] * f);
       }
+    if (tid < RB) {
+      float mm = kNoMax, ll = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w][tid]);
+#pragma unroll 4
+      for (int w = 0; w < W; ++w) ll += s_l[w][tid] * ex2(s_m[w][tid] - mm);
+      s_mm[tid] = mm;
+      s_ll[tid] = ll;
+    }
     __syncthreads();
-    const bool whole = k0 == 0 && k1 == n_ch;
-    const int side = k0 > 0 ? 0 : 1;
-    float* part = a.partial + ((size_t)blockIdx.x * 2 + side) * a.part_stride;
-    const float vts = a.cache.v_ts ? a.cache.v_ts[h] : 1.0f;
-    for (int i = tid; i < RB * (D / 4); i += kDecThreads) {
-      const int row = i / (D / 4), d4 = i - row * (D / 4);
+    float* part_out = a.partial + ((size_t)blockIdx.x * 2 + (it.k0 > 0 ? 0 : 1)) * a.part_stride;
+#pragma unroll 1
+    for (int i = tid; i < RB * (D / 4); i += THREADS) {
+      const int row = i / (D / 4), q = i - row * (D / 4);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float4 v = reinterpret_cast<const float4*>(s_o + ((size_t)w * RB + row) * D)[d4];
+#pragma unroll 4
+      for (int w = 0; w < W; ++w) {
+        const float4 v = reinterpret_cast<const float4*>(s_o + (w * RB + row) * (D + 8))[q];
         acc.x += v.x;
         acc.y += v.y;
         acc.z += v.z;
         acc.w += v.w;
       }
       if (whole) {
-        const int rr = row_first + row;
-        if (rr < rows) {
-          const int tok = rr / a.G, head = h * a.G + rr - tok * a.G;
-          const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
-          const float ll = s_ll[row], f = ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
-          const __nv_bfloat162 p0 = __floats2bfloat162_rn(acc.x * f, acc.y * f),
-                               p1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-          *reinterpret_cast<uint2*>(a.out + out_row * D + d4 * 4) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
-          if (a.lse && d4 == 0) a.lse[out_row] = ll == 0.0f ? -INFINITY : (s_mm[row] + log2f(ll)) * kLn2;
-        }
+        if (row_first + row < rows) write_row<D>(a, it.sq, h, row_first + row, q, acc, s_mm[row], s_ll[row], vts);
       } else {
-        reinterpret_cast<float4*>(part + 2 * RB)[i] = acc;
-        if (d4 == 0) {
-          part[row] = s_mm[row];
-          part[RB + row] = s_ll[row];
+        reinterpret_cast<float4*>(part_out + 2 * RB)[i] = acc;
+        if (q == 0) {
+          part_out[row] = s_mm[row];
+          part_out[RB + row] = s_ll[row];
         }
       }
     }
-    if (!whole && side == 1 && tid == 0) {
+    if (!whole && it.k0 == 0 && tid == 0) {
       // the blocks after this one that hold the rest of the item
-      const long long item_end = at + (n_ch - k1);
+      const long long end = it.at + (it.n_ch - it.k1);
       int last = blockIdx.x + 1;
-      while (total * (last + 1) / grid < item_end) ++last;
-      a.meta[blockIdx.x] = make_int4(b, h, row_first, last);
+      while (total * (last + 1) / grid < end) ++last;
+      a.meta[blockIdx.x] = make_int4(it.b, h, row_first, last);
     }
     __syncthreads();
+    if (more) {
+      it = coming;
+      if (!kApart) {
+        fence_proxy_async_smem();  // the ring's next copies come after these reads and writes of it
+        __syncthreads();
+      }
+    }
   }
 }
 
-// One block per (run that ends inside an item, row): joins the item's partial results.
+// One block per (run that ends inside an item, row): joins the item's parts, eight loads at a time.
 template <int D, int RB>
 __global__ void __launch_bounds__(D / 4) kv_attn_join_kernel(const KvAttnArgs a) {
   MOE_PDL_PROLOGUE();
-  const int4 meta = a.meta[blockIdx.x];
+  const int first = blockIdx.x, row = blockIdx.y, q = threadIdx.x;
+  const int4 meta = a.meta[first];
   if (meta.x < 0) return;
   const SeqSpan sq = load_seq(a, meta.x);
-  const int row = blockIdx.y, rr = meta.z + row;
-  if (rr >= sq.n_q * a.G) return;
-  const int first = blockIdx.x, last = meta.w;
-  auto part = [&](int i) { return a.partial + ((size_t)i * 2 + (i == first ? 1 : 0)) * a.part_stride; };
-  float mm = kNoMax;
-  for (int i = first; i <= last; ++i) mm = fmaxf(mm, part(i)[row]);
-  float ll = 0.0f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = first; i <= last; ++i) {
-    const float* p = part(i);
-    const float f = ex2(p[row] - mm);
-    ll += p[RB + row] * f;
-    const float4 v = reinterpret_cast<const float4*>(p + 2 * RB)[row * (D / 4) + threadIdx.x];
-    acc.x += v.x * f;
-    acc.y += v.y * f;
-    acc.z += v.z * f;
-    acc.w += v.w * f;
-  }
-  const int tok = rr / a.G, head = meta.y * a.G + rr - tok * a.G;
-  const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
+  const int rr = meta.z + row, last = meta.w;
   const float vts = a.cache.v_ts ? a.cache.v_ts[meta.y] : 1.0f;
-  const float f = ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
-  const __nv_bfloat162 p0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), p1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-  *reinterpret_cast<uint2*>(a.out + out_row * D + threadIdx.x * 4) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
-  if (a.lse && threadIdx.x == 0) a.lse[out_row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  float mm = kNoMax, ll = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int j0 = first; j0 <= last; j0 += 8) {
+    float pm[8], pl[8];
+    float4 pv[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = min(j0 + j, last);
+      const float* p = a.partial + ((size_t)k * 2 + (k == first ? 1 : 0)) * a.part_stride;
+      pm[j] = p[row];
+      pl[j] = p[RB + row];
+      pv[j] = reinterpret_cast<const float4*>(p + 2 * RB + row * D)[q];
+    }
+    float top = mm;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, pm[j]);
+    const float f0 = ex2(mm - top);
+    mm = top;
+    ll *= f0;
+    acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = j0 + j <= last ? ex2(pm[j] - top) : 0.0f;  // (past the last: the last again, not counted)
+      ll += pl[j] * f;
+      acc.x += pv[j].x * f;
+      acc.y += pv[j].y * f;
+      acc.z += pv[j].z * f;
+      acc.w += pv[j].w * f;
+    }
+  }
+  if (rr < sq.n_q * a.G) write_row<D>(a, sq, meta.y, rr, q, acc, mm, ll, vts);
 }
 
-constexpr int dec_smem(int D, int NR) { return kDecWarps * 8 * NR * D * 4; }
-constexpr int dec_blocks(int D, int NR) { return D == 256 || NR > 1 ? 1 : 2; }  // blocks of an SM
-
 template <int D, int NR>
-cudaError_t launch_dec(KvAttnArgs a, int num_sms, cudaStream_t st) {
+cudaError_t launch_dec(const KvAttnArgs& a, int num_sms, cudaStream_t st) {
   const int grid = num_sms * dec_blocks(D, NR);
-  cudaError_t e = launch_pdl(kv_attn_dec_kernel<D, NR>, dim3(grid), dim3(kDecThreads), dec_smem(D, NR), st, a);
+  cudaError_t e = launch_pdl(kv_attn_dec_kernel<D, NR>, dim3(grid), dim3(32 * dec_warps(D, NR)), dec_smem(D, NR), st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_attn_join_kernel<D, 8 * NR>, dim3(grid, 8 * NR), dim3(D / 4), 0, st, a);
 }
@@ -526,6 +618,8 @@ cudaError_t attributes_dec() {
 }  // namespace
 
 size_t kv_attn_dec_part_floats(int D) { return 16 * (size_t)(D + 2); }
+
+cudaError_t set_wait_limit_kv_attn_dec(unsigned long long ns) { return set_wait_limit_here(ns); }
 
 cudaError_t init_kv_attn_dec_attributes() {
   cudaError_t e = attributes_dec<64>();

@@ -231,27 +231,6 @@ MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// mbar_wait with the limit read once per block: short in code (the roles of a block share the
-// instruction caches) and without a load from global memory in every wait.
-struct Patience {
-  volatile int abort;
-  unsigned long long limit;
-};
-MOE_DEV bool wait_soon(uint64_t* bar, uint32_t parity, Patience* w, int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (w->abort) return false;
-    if (globaltimer_ns() - t0 > w->limit) {
-      w->abort = 1;
-      atomicExch(status, kStatusTimeout);
-      return false;
-    }
-  }
-  return true;
-}
-
 // Waits for two barriers at once, every other lane for the second (a wait that is over at once
 // still costs the round trip). For a whole warp; the same answer in all lanes.
 MOE_DEV bool wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1, Patience* w, int32_t* status) {
