@@ -101,13 +101,18 @@ MOE_DEV uint32_t load_scales(const uint8_t* src) {
   return *reinterpret_cast<const uint32_t*>(src);
 }
 
+// What the start and end of an item cost a block (queries, first keys, joining the warps), in
+// chunks: 8 us of 0.5 us at D = 256, 4 us of 0.55 us below. Every block starts one item; the cost
+// counts the further ones.
+__host__ __device__ constexpr int start_chunks(int D) { return D == 256 ? 16 : 7; }
+
 MOE_DEV int seq_chunks(const SeqSpan& s) { return max(1, (s.ctx + kChunk - 1) / kChunk); }
 
-// Chunks of all items of a sequence; 0 for one that this kernel leaves to the other.
-MOE_DEV int64_t seq_cost(const KvAttnArgs& a, const SeqSpan& s, int rows_per_group) {
+// Work of all items of a sequence (chunks and starts); 0 for one that this kernel leaves to the other.
+MOE_DEV int64_t seq_cost(const KvAttnArgs& a, const SeqSpan& s, int rows_per_group, int start) {
   const int rows = s.n_q * a.G;
   if (rows == 0 || rows > a.dec_max_rows) return 0;
-  return (int64_t)seq_chunks(s) * a.cache.Hkv * ((rows + rows_per_group - 1) / rows_per_group);
+  return (int64_t)(seq_chunks(s) + start) * a.cache.Hkv * ((rows + rows_per_group - 1) / rows_per_group);
 }
 
 // Rows of outputs are kept in the order of the fragments: place 16 i + 2 g + e holds element
@@ -127,13 +132,13 @@ MOE_DEV void write_row(const KvAttnArgs& a, const SeqSpan& sq, int h, int rr, in
 struct Item {
   SeqSpan sq;
   int b, h, row_first, k0, k1, n_ch;
-  long long at;  // its end, counted in chunks over all items
+  long long end;  // where the item's work ends, counted over all items
 };
 
 template <int D, int NR>
 __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_attn_dec_kernel(const KvAttnArgs a) {
   constexpr int RB = 8 * NR, W = dec_warps(D, NR), THREADS = 32 * W;
-  constexpr int KSTEPS = D / 16;
+  constexpr int KSTEPS = D / 16, start = start_chunks(D);
   constexpr int KW = D / 32, VW = D / 64;  // words of codes that a thread holds of a K row, of a V row
   constexpr int KS = D / 64, VS = D >= 128 ? D / 128 : 1;  // bytes of scales
   // a stage: codes of K, codes of V, scales of K, scales of V
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
   SeqSpan one = {};  // of a thread with one sequence, read once
   for (int b = b_lo; b < b_hi; ++b) {
     one = load_seq(a, b);
-    mine += seq_cost(a, one, RB);
+    mine += seq_cost(a, one, RB, start);
   }
   long long incl = mine;
 #pragma unroll
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
     total += s_scan[w];
   }
   before += incl - mine;
-  const int grid = (int)min((long long)gridDim.x, total);  // blocks that get any; each of them at least one chunk
+  const int grid = (int)min((long long)gridDim.x, total);  // blocks that get any
   if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if ((int)blockIdx.x >= grid) return;
   const long long c_begin = total * blockIdx.x / grid, c_end = total * (blockIdx.x + 1) / grid;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
     long long at = before;
     for (int b = b_lo; b < b_hi; ++b) {
       const SeqSpan sq = per == 1 ? one : load_seq(a, b);
-      const long long cost = seq_cost(a, sq, RB);
+      const long long cost = seq_cost(a, sq, RB, start);
       if (c_begin < at + cost) {
         s_seq = sq;
         s_b = b;
@@ -219,15 +224,17 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
   SeqSpan sq = s_seq;
   auto next_item = [&](Item* it) {
     while (at < c_end && b < a.n_seqs) {
-      const long long cost = seq_cost(a, sq, RB);
+      const long long cost = seq_cost(a, sq, RB, start);
       if (local < cost) {
-        const int n_ch = seq_chunks(sq), n_rg = (sq.n_q * a.G + RB - 1) / RB;
-        const int item = (int)(local / n_ch), k0 = (int)(local - (long long)item * n_ch);
-        const int k1 = (int)min((long long)n_ch, k0 + c_end - at);
-        local += k1 - k0;
-        at += k1 - k0;
-        *it = Item{sq, b, item / n_rg, item % n_rg * RB, k0, k1, n_ch, at};
-        return true;
+        const int n_ch = seq_chunks(sq), n_rg = (sq.n_q * a.G + RB - 1) / RB, cost1 = n_ch + start;
+        const int item = (int)(local / cost1), lo = (int)(local - (long long)item * cost1);
+        const int hi = (int)min((long long)cost1, lo + c_end - at);
+        const int k0 = max(0, lo - start), k1 = max(0, hi - start);
+        local += hi - lo;
+        at += hi - lo;
+        *it = Item{sq, b, item / n_rg, item % n_rg * RB, k0, k1, n_ch, at + cost1 - hi};
+        if (k1 > k0) return true;
+        continue;
       }
       local = 0;
       if (++b < a.n_seqs) sq = load_seq(a, b);
@@ -539,9 +546,8 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
     }
     if (!whole && it.k0 == 0 && tid == 0) {
       // the blocks after this one that hold the rest of the item
-      const long long end = it.at + (it.n_ch - it.k1);
       int last = blockIdx.x + 1;
-      while (total * (last + 1) / grid < end) ++last;
+      while (total * (last + 1) / grid < it.end) ++last;
       a.meta[blockIdx.x] = make_int4(it.b, h, row_first, last);
     }
     __syncthreads();
