@@ -339,7 +339,8 @@ typedef struct moe_kv_cache {
  *                       [0, D]; 0 for no rotation (inv_freq and positions may then be NULL)
  *   interleaved         0: pairs (p, p + rot_dim/2); else pairs (2p, 2p + 1)
  *   rot_scale           factor on sine and cosine (1 unless the frequency scaling has one)
- * Computed in float64, rounded to float32 and then to bf16.
+ * Keys are computed in float64 and rounded to float32 and then to bf16; queries in float32 with
+ * the sines and cosines from float64 angles.
  */
 typedef struct moe_qk_prep {
   const float* q_weight;

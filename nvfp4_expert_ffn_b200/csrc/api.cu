@@ -640,6 +640,7 @@ moe_status nvfp4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* 
   set_prep(&a, *prep, positions);
   a.slots = slots;
   a.cache = to_cache(*cache);
+  while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
   a.q_out = q_out;
   a.status = dstatus;
   cudaError_t e = launch_qkv_prep(a, cache->D, sms, (cudaStream_t)stream);

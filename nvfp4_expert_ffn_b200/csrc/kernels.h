@@ -203,6 +203,7 @@ struct QkvPrepArgs {
   double rot_scale;
   const int32_t* slots;  // NULL: nothing is cached
   KvCacheArgs cache;
+  int page_shift;
   uint16_t *q_out, *k_out;
   int32_t* status;
 };

@@ -57,10 +57,15 @@ def test_norm_rope(D, Hq, Hkv, rot, inter, T):
     qv, kv = fused[:, :Hq * D].unflatten(1, (Hq, D)), fused[:, Hq * D:].unflatten(1, (Hkv, D))
     qo, ko = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
     B.moe_qk_norm_rope(qv, kv, _gpu(pos), prep, qo, ko)
-    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+    for got, x, w, steps in ((qo, q, qw, 8), (ko, k, kw, 0)):
         ref = okv.norm_rope(x, pos, w, 1e-5, f if rot else None, inter, m)
-        # float64 all the way to the roundings: half a bf16 step and half a float32 step
-        assert np.all(np.abs(_np(got) - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -23) + 1e-37)
+        # keys are float64 all the way to the roundings: half a bf16 step and half a float32 step.
+        # Queries are float32: the factor (a sum of D squares, D / 8 in a row, then log2 of the lanes:
+        # at most 13 steps; divide, add, root, reciprocal), two products and a sum of two rotated
+        # terms, so D / 16 + 8 steps of 2^-24 of the pair's size times m
+        pair = 0.0 if steps == 0 else 2.0 ** -24 * (D / 16 + 16) * m * np.sqrt(2) * np.abs(
+            okv.norm_rope(np.abs(x), pos, np.abs(w), 1e-5)).max(axis=-1, keepdims=True)
+        assert np.all(np.abs(_np(got) - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -23) + pair + 1e-37)
     # in place, from contiguous rows, one side at a time
     qc, kc = qv.contiguous(), kv.contiguous()
     B.moe_qk_norm_rope(qc, None, _gpu(pos), prep, qc, None)
