@@ -19,56 +19,78 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv_attn.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kPrepThreads = 256;
-constexpr int kPrepTokens = 4;  // tokens of a block when there are many: 64 pairs each fill its threads
+// Many tokens: blocks of four warps, each with a token of its own, whose rows it walks over with
+// constant strides. Few: a block of eight warps for every token.
+constexpr int kManyWarps = 4, kFewWarps = 8;
 
-// Two lanes hold a block of 16 (8 elements each); amax is the block's, signs the sign bits of the
-// elements where their codes have them. The codes of quantize_block16 (common.cuh): E2M1 of the
-// correctly rounded quotients x / denom. Those come from one reciprocal per block by Markstein's
-// theorem (P. Markstein, IBM J. Res. Dev. 34, 1990): with y the correctly rounded 1 / d,
-// q = x y, r = x - q d (exact in a fused step), q + r y is the correctly rounded x / d, unless
-// d's significand is all ones, or a step over- or underflows. Blocks where that could be are
-// divided (an underflow of x y is none: the code is 0 either way).
-MOE_DEV uint32_t quantize_half16(const float (&v)[8], uint32_t signs, float amax, float ts, uint32_t* codes) {
-  const uint32_t s = f32_to_e4m3_sat(__fdiv_rn(__fdiv_rn(amax, kE2M1Max), ts));
-  const float sval = e4m3_to_f32(s);
-  *codes = 0;
-  if (sval == 0.0f) return s;
-  const float d = __fmul_rn(sval, ts);
-  float q[8];
-  if (d > 0x1p-60f && d < 0x1p60f && amax < 0x1p60f && (__float_as_uint(d) & 0x7FFFFFu) != 0x7FFFFFu) {
-    const float y = __frcp_rn(d);
+MOE_DEV void unpack8x2(const uint4& p, uint64_t (&v)[4]) {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = fabsf(v[i]), q0 = __fmul_rn(x, y);
-      q[i] = __fmaf_rn(__fmaf_rn(-q0, d, x), y, q0);
+  for (int i = 0; i < 4; ++i) v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+// Quotients by Markstein's theorem (P. Markstein, IBM J. Res. Dev. 34, 1990): with y the
+// correctly rounded 1 / d, q = x y, r = x - q d (exact in a fused step), q + r y is the correctly
+// rounded x / d, unless d's significand is all ones, or a step over- or underflows.
+MOE_DEV bool good_divisor(float d) {
+  return d > 0x1p-60f && d < 0x1p60f && (__float_as_uint(d) & 0x7FFFFFu) != 0x7FFFFFu;
+}
+MOE_DEV float quotient(float x, float d, float y) {
+  const float q = __fmul_rn(x, y);
+  return __fmaf_rn(__fmaf_rn(-q, d, x), y, q);
+}
+
+// Two lanes hold a block of 16 (8 elements each); amax is the block's, y the correctly rounded
+// 1 / ts. The scale and codes of quantize_block16 (common.cuh): E2M1 of the correctly rounded
+// x / denom. Blocks that the theorem does not cover are divided (an underflow on the way is none:
+// the result is 0 either way). The sign is x's own: that of a zero is lost on the way.
+MOE_DEV uint32_t quantize_half16(const uint4& p, float amax, float ts, float y, uint32_t* codes) {
+  const bool good = good_divisor(ts) && amax < 0x1p60f;
+  const float sb = good ? quotient(quotient(amax, kE2M1Max, 1.0f / kE2M1Max), ts, y) : __fdiv_rn(__fdiv_rn(amax, kE2M1Max), ts);
+  const uint32_t s = f32_to_e4m3_sat(sb);
+  *codes = 0;
+  if (s == 0) return s;
+  const float d = __fmul_rn(__half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(s))), ts);
+  uint64_t v[4];
+  unpack8x2(p, v);
+  float q[8];
+  if (good && good_divisor(d)) {
+    const float yd = __frcp_rn(d);
+    const uint64_t y2 = pack2(yd, yd), d2 = pack2(-d, -d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t q0 = mul2(v[i], y2);
+      unpack2(fma2(fma2(q0, d2, v[i]), y2, q0), q[2 * i], q[2 * i + 1]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = fabsf(__fdiv_rn(v[i], d));
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack2(v[i], lo, hi);
+      q[2 * i] = __fdiv_rn(lo, d);
+      q[2 * i + 1] = __fdiv_rn(hi, d);
+    }
   }
-  uint32_t c = signs;
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 q;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\tcvt.u32.u8 %0, q;\n\t}" : "=r"(r) : "f"(q[2 * i]), "f"(q[2 * i + 1]));
-    c |= r << (8 * i);
+    q[2 * i] = __uint_as_float((__float_as_uint(q[2 * i]) & 0x7FFFFFFFu) | ((w[i] << 16) & 0x80000000u));
+    q[2 * i + 1] = __uint_as_float((__float_as_uint(q[2 * i + 1]) & 0x7FFFFFFFu) | (w[i] & 0x80000000u));
   }
-  *codes = c;
-  return s;
-}
-
-// sign bits of 8 packed bf16 values, at bit 4 i + 3 for element i
-MOE_DEV uint32_t sign_bits(const uint4& p) {
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-  uint32_t s = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s |= (((w[i] >> 12) & 0x8u) | ((w[i] >> 24) & 0x80u)) << (8 * i);
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(*codes)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
   return s;
 }
 
@@ -81,12 +103,18 @@ MOE_DEV void unpack8(const uint4& p, float (&v)[8]) {
   }
 }
 
-// (weights need 4-byte alignment only)
-MOE_DEV float4 ldg4(const float* p) { return make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3)); }
-
 MOE_DEV uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// An angle less its whole turns, 2 pi in two parts (Cody and Waite): exact to 2^-50 up to 2^40
+// radians. The library's own reduction of arguments beyond 10^5 takes a slow path.
+MOE_DEV double whole_turns_off(double t) {
+  constexpr double kTurn = 6.283185307179586, kTurnLow = 2.4492935982947064e-16;
+  if (!(fabs(t) < 0x1p40)) return t;
+  const double k = rint(t * (1.0 / kTurn));
+  return fma(-k, kTurnLow, fma(-k, kTurn, t));
 }
 
 // A row's norm factor from its sum of squares: one Newton step in float64 from the float32
@@ -98,187 +126,245 @@ MOE_DEV double norm_factor(double ss, int D, double eps) {
   return y * (1.5 - 0.5 * x * y * y);
 }
 
+// A bf16 of a packed pair as float64, 2^-896 of it: the exponent's bits are only moved, zeros
+// and subnormals included, in a quarter of a conversion's time. (Infinities and NaN become
+// numbers.)
+constexpr double kUp = 0x1p896;
+MOE_DEV double widen(uint32_t w, int high) {
+  const uint32_t hi = high ? ((w & 0x7FFF0000u) >> 3) | (w & 0x80000000u) : ((w & 0x7FFFu) << 13) | ((w & 0x8000u) << 16);
+  return __hiloint2double((int)hi, 0);
+}
+
+// Calls body(row's 16 bytes, head, live) for the heads first + sub, first + step + sub, ... of a
+// token, PF rows' loads under way: one row at a time leaves most of the memory's latency
+// uncovered.
+template <int PF, typename Body>
+MOE_DEV void each_row(const uint16_t* x, int heads, int first, int sub, int step, int D, int e0, Body body) {
+  const uint16_t* src = x + (first + sub) * D + e0;
+  int ahead = first + sub;
+  uint4 p[PF];
+  auto load = [&]() {
+    const uint4 v = ahead < heads ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+    ahead += step;
+    src += step * D;
+    return v;
+  };
+#pragma unroll
+  for (int i = 0; i < PF; ++i) p[i] = load();
+#pragma unroll 1
+  for (int h = first; h < heads;) {
+#pragma unroll
+    for (int i = 0; i < PF; ++i) {
+      if (h >= heads) break;
+      const uint4 v = p[i];
+      p[i] = load();
+      body(v, h + sub, h + sub < heads);
+      h += step;
+    }
+  }
+}
+
 // D/8 lanes a head row, 16 bytes a lane; a warp takes 32 * 8 / D rows of one kind (key, value or
-// query) at a time. A block takes `tokens` tokens and all their rows, so that the sines and
-// cosines of a token are computed once for all its heads.
+// query) at a time. Weight, sine and cosine of a token's elements are the same for all its heads:
+// element e of a row becomes (x_e A_e + x_partner B_e) * norm factor, with A = w cos and B = -/+ w
+// of the partner * sin, in tables that a block builds for its `tokens` tokens. The tables are
+// turned (element 8 lane + i at row i, column lane), so that lanes read words side by side.
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads) qkv_prep_kernel(const QkvPrepArgs a, int tokens) {
+__global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPrepArgs a, int tokens) {
   MOE_PDL_PROLOGUE();
   constexpr int L = D / 8;      // lanes of a row
   constexpr int RPW = 32 / L;   // rows of a warp
-  __shared__ double s_cos[kPrepTokens][D / 2], s_sin[kPrepTokens][D / 2];
-  __shared__ float s_cosf[kPrepTokens][D / 2], s_sinf[kPrepTokens][D / 2];
+  constexpr int NT = kManyWarps;
+  const int threads = blockDim.x;
+  __shared__ __align__(16) double s_ka[NT][D], s_kb[NT][D];
+  __shared__ __align__(16) float s_qa[NT][D], s_qb[NT][D];
   const int t0 = blockIdx.x * tokens;
   const int nt = min(tokens, a.T - t0);
   const int half = a.rot / 2;
-  const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31, lane = wl % L, e0 = lane * 8;
-  // a block's rows: units of RPW rows, keys first (they take longest), then values, then queries
-  const int nk = (nt * a.Hk + RPW - 1) / RPW, nv = (nt * a.Hv + RPW - 1) / RPW, nq = (nt * a.Hq + RPW - 1) / RPW;
-  const int units = nk + nv + nq;
-  auto source = [&](int u, int* kind, int* t, int* h, bool* live) -> uint4 {
-    *kind = u < nk ? 1 : u < nk + nv ? 2 : 0;
-    const int heads = *kind == 1 ? a.Hk : *kind == 2 ? a.Hv : a.Hq;
-    const int row = (u - (*kind == 1 ? 0 : *kind == 2 ? nk : nk + nv)) * RPW + wl / L;
-    *live = u < units && row < nt * heads;
-    *t = *live ? row / heads : 0;
-    *h = *live ? row - *t * heads : 0;
-    const uint16_t* x = *kind == 1 ? a.k : *kind == 2 ? a.v : a.q;
-    const int64_t stride = *kind == 1 ? a.k_stride : *kind == 2 ? a.v_stride : a.q_stride;
-    return *live ? *reinterpret_cast<const uint4*>(x + (int64_t)(t0 + *t) * stride + (int64_t)*h * D + e0)
-                 : make_uint4(0u, 0u, 0u, 0u);
-  };
-  int kind, t, h, kind_n, t_n, h_n;
-  bool live, live_n;
-  uint4 p_n = source(warp, &kind_n, &t_n, &h_n, &live_n);  // a unit ahead
-  for (int i = threadIdx.x; i < nt * half; i += kPrepThreads) {
-    const int ti = i / half, p = i - ti * half;
+  const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31, lane = wl % L, sub = wl / L, e0 = lane * 8;
+  auto at_k = [](int e) { return (e & 7) * L + (e >> 3); };
+  auto at_q = [](int e) { return (((e & 7) >> 1) * L + (e >> 3)) * 2 + (e & 1); };
+  for (int i = threadIdx.x; i < nt * half; i += threads) {
+    const int t = i / half, p = i - t * half;
+    const int lo = a.interleaved ? 2 * p : p, hi = a.interleaved ? 2 * p + 1 : p + half;
     double sn, cs;
-    sincos((double)a.positions[t0 + ti] * (double)a.inv_freq[p], &sn, &cs);
-    s_cos[ti][p] = cs * a.rot_scale;
-    s_sin[ti][p] = sn * a.rot_scale;
-    s_cosf[ti][p] = (float)(cs * a.rot_scale);
-    s_sinf[ti][p] = (float)(sn * a.rot_scale);
+    sincos(whole_turns_off((double)a.positions[t0 + t] * (double)a.inv_freq[p]), &sn, &cs);
+    sn *= a.rot_scale;
+    cs *= a.rot_scale;
+    if (a.Hq) {
+      const double wl = a.q_weight ? (double)a.q_weight[lo] : 1.0, wh = a.q_weight ? (double)a.q_weight[hi] : 1.0;
+      s_qa[t][at_q(lo)] = (float)(wl * cs);
+      s_qa[t][at_q(hi)] = (float)(wh * cs);
+      s_qb[t][at_q(lo)] = (float)(-wh * sn);
+      s_qb[t][at_q(hi)] = (float)(wl * sn);
+    }
+    if (a.Hk) {
+      const double wl = a.k_weight ? (double)a.k_weight[lo] : 1.0, wh = a.k_weight ? (double)a.k_weight[hi] : 1.0;
+      s_ka[t][at_k(lo)] = wl * cs;
+      s_ka[t][at_k(hi)] = wh * cs;
+      s_kb[t][at_k(lo)] = -wh * sn * kUp;
+      s_kb[t][at_k(hi)] = wl * sn * kUp;
+    }
+  }
+  const int rest = D - a.rot;  // elements that are not turned
+  for (int i = threadIdx.x; i < nt * rest; i += threads) {
+    const int t = i / rest, e = a.rot + i - t * rest;
+    if (a.Hq) s_qa[t][at_q(e)] = a.q_weight ? a.q_weight[e] : 1.0f;
+    if (a.Hk) s_ka[t][at_k(e)] = a.k_weight ? (double)a.k_weight[e] : 1.0;
   }
   __syncthreads();
-  const int n_slots = a.cache.n_pages * a.cache.page_size;
-  // the partner of a half-split pair sits R/16 lanes away
-  const int hop = half / 8;
-  const bool lower = e0 < half, turned = e0 < a.rot;
-  const int from = (lower ? lane + hop : lane - hop) & (L - 1), from_lane = (wl - lane) + from;
-  const int pe = from * 8, p0 = a.interleaved ? e0 / 2 : lower ? e0 : e0 - half;
-#pragma unroll 1
-  for (int u = warp; u < units; u += kPrepThreads / 32) {
-    uint4 p = p_n;
-    kind = kind_n; t = t_n; h = h_n; live = live_n;
-    p_n = source(u + kPrepThreads / 32, &kind_n, &t_n, &h_n, &live_n);
-    float y[8];
-    unpack8(p, y);
-    float q[8];
-    if (kind != 2 && !a.interleaved && half) {
-      uint4 pp;
-      pp.x = __shfl_sync(0xffffffffu, p.x, from_lane);
-      pp.y = __shfl_sync(0xffffffffu, p.y, from_lane);
-      pp.z = __shfl_sync(0xffffffffu, p.z, from_lane);
-      pp.w = __shfl_sync(0xffffffffu, p.w, from_lane);
-      unpack8(pp, q);
+  // the partner of a half-split pair sits half a rotation away; of an interleaved one, beside it
+  const bool turned = e0 < a.rot, hop = !a.interleaved && half;
+  const int from_lane = (wl - lane) + (!turned ? lane : e0 < half ? lane + half / 8 : lane - half / 8);
+  auto partner = [&](const uint4& p) {
+    return make_uint4(__shfl_sync(0xffffffffu, p.x, from_lane), __shfl_sync(0xffffffffu, p.y, from_lane),
+                      __shfl_sync(0xffffffffu, p.z, from_lane), __shfl_sync(0xffffffffu, p.w, from_lane));
+  };
+  auto beside = [](const uint4& p) {
+    return make_uint4(__funnelshift_l(p.x, p.x, 16), __funnelshift_l(p.y, p.y, 16), __funnelshift_l(p.z, p.z, 16),
+                      __funnelshift_l(p.w, p.w, 16));
+  };
+  // this warp's token, and its share of the token's rows
+  const bool many = tokens > 1;
+  const int t = many ? warp : 0, tok = t0 + t;
+  if (t >= nt) return;
+  const int step = RPW * (many ? 1 : threads / 32);
+  // (with a block to a token the kinds start at different warps, to keep all of them busy)
+  const int nk = (a.Hk + RPW - 1) / RPW, nv = (a.Hv + RPW - 1) / RPW;
+  auto first = [&](int before) { return many ? 0 : ((warp - before) & (kFewWarps - 1)) * RPW; };
+  int64_t cache_row = -1;  // the token's cache row of head 0
+  if (a.slots) {
+    const int slot = a.slots[tok], n_slots = a.cache.n_pages * a.cache.page_size;
+    if (slot >= n_slots) atomicExch(a.status, kStatusInvalid);
+    if (slot >= 0 && slot < n_slots)
+      cache_row = (int64_t)(slot >> a.page_shift) * a.cache.Hkv * a.cache.page_size + (slot & (a.cache.page_size - 1));
+  }
+  // the quantised write of a lane's 8 elements of a key or value (p: packed bf16)
+  auto store = [&](const uint4& p, int h, bool live, const float* tsp, uint8_t* codes, uint8_t* scales) {
+    uint32_t m = (p.x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, p.y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, p.z & 0x7FFF7FFFu);
+    m = __vmaxu2(m, p.w & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if (m > 0x7F80u) {  // NaN: the largest of the numbers beside it
+      float top = 0.0f, v[8];
+      unpack8(p, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+      m = __float_as_uint(fmaxf(top, __shfl_xor_sync(3u << (wl & ~1), top, 1))) >> 16;
     }
-    if (kind == 0) {
-      // ---- a query, in float32
-      if (a.q_weight) {
-        float ss = 0.0f;
+    if (!live || cache_row < 0) return;
+    const float ts = tsp ? __ldg(tsp + h) : 1.0f;
+    uint32_t c;
+    const uint32_t s = quantize_half16(p, bf16_to_f32(m), ts, __frcp_rn(ts), &c);
+    const int64_t row = cache_row + (int64_t)h * a.cache.page_size;
+    *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + e0 / 2) = c;
+    if ((lane & 1) == 0) scales[row * (D / 16) + e0 / 16] = (uint8_t)s;
+  };
+
+  // ---- keys, in float64
+  if (a.Hk) each_row<2>(a.k + tok * a.k_stride, a.Hk, first(0), sub, step, D, e0, [&](uint4 p, int h, bool live) {
+    const uint4 pp = hop ? partner(p) : beside(p);
+    if (a.k_weight || turned) {
+      uint32_t x[4] = {p.x, p.y, p.z, p.w};
+      const uint32_t xp[4] = {pp.x, pp.y, pp.z, pp.w};
+      double v[8], rs = 1.0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+      for (int i = 0; i < 8; ++i) v[i] = widen(x[i >> 1], i & 1) * kUp;
+      uint32_t m = __vmaxu2(__vmaxu2(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu), __vmaxu2(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu));
+      const bool special = max(m & 0xFFFFu, m >> 16) >= 0x7F80u;
+      if (special) {  // (an infinity counts as the NaN that the norm or the rotation makes of it)
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        float rs = 1.0f / sqrtf(ss / D + (float)a.eps);
-        const bool far = !(ss < 1e36f && ss > 1e-30f);  // squares near the ends of float32's range
-        if (__any_sync(0xffffffffu, far)) {
-          double sd = 0.0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sd = fma((double)y[i], (double)y[i], sd);
-#pragma unroll
-          for (int o = L / 2; o > 0; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-          if (far) {
-            const double r = norm_factor(sd, D, a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              y[i] = (float)(y[i] * r);
-              if (turned && !a.interleaved) q[i] = (float)(q[i] * r);
-            }
-            rs = 1.0f;
-          }
-        }
-        const float4 w0 = ldg4(a.q_weight + e0), w1 = ldg4(a.q_weight + e0 + 4);
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= rs * w[i];
-        if (turned && !a.interleaved) {
-          const float4 x0 = ldg4(a.q_weight + pe), x1 = ldg4(a.q_weight + pe + 4);
-          const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] *= rs * x[i];
-        }
+        for (int i = 0; i < 8; ++i)
+          if (((x[i >> 1] >> (16 * (i & 1))) & 0x7F80u) == 0x7F80u) v[i] = __longlong_as_double(0x7FF8000000000000ll);
       }
-      if (turned) {
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float c = s_cosf[t][p0 + i], s = s_sinf[t][p0 + i], lo = y[2 * i], hi = y[2 * i + 1];
-            y[2 * i] = lo * c - hi * s;
-            y[2 * i + 1] = hi * c + lo * s;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float c = s_cosf[t][p0 + i], s = s_sinf[t][p0 + i];
-            y[i] = lower ? y[i] * c - q[i] * s : y[i] * c + q[i] * s;
-          }
-        }
-      }
-      if (live)
-        *reinterpret_cast<uint4*>(a.q_out + ((int64_t)(t0 + t) * a.Hq + h) * D + e0) =
-            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-      continue;
-    }
-    if (kind == 1) {
-      // ---- a key, in float64
-      double rs = 1.0;
       if (a.k_weight) {
         double ss = 0.0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fma((double)y[i], (double)y[i], ss);
+        for (int i = 0; i < 8; ++i) ss = fma(v[i], v[i], ss);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         rs = norm_factor(ss, D, a.eps);
       }
-      double z[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = a.k_weight ? (double)y[i] * rs * (double)__ldg(a.k_weight + e0 + i) : (double)y[i];
-      if (turned) {
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const double c = s_cos[t][p0 + i], s = s_sin[t][p0 + i], lo = z[2 * i], hi = z[2 * i + 1];
-            z[2 * i] = lo * c - hi * s;
-            z[2 * i + 1] = hi * c + lo * s;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const double o = a.k_weight ? (double)q[i] * rs * (double)__ldg(a.k_weight + pe + i) : (double)q[i];
-            const double c = s_cos[t][p0 + i], s = s_sin[t][p0 + i];
-            z[i] = lower ? z[i] * c - o * s : z[i] * c + o * s;
-          }
-        }
+      for (int i = 0; i < 8; ++i) {
+        double z = v[i] * s_ka[t][i * L + lane];
+        if (turned) z = fma(widen(xp[i >> 1], i & 1), s_kb[t][i * L + lane], z);
+        v[i] = z * rs;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = (float)z[i];
-      p = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-      if (live && a.k_out) *reinterpret_cast<uint4*>(a.k_out + ((int64_t)(t0 + t) * a.Hk + h) * D + e0) = p;
-      if (!a.slots) continue;
-      unpack8(p, y);
+      for (int i = 0; i < 4; ++i) x[i] = pack_bf16((float)v[2 * i], (float)v[2 * i + 1]);
+      p = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    // ---- the quantised write of a key or value
-    float amax = 0.0f;
+    if (live && a.k_out) *reinterpret_cast<uint4*>(a.k_out + ((int64_t)tok * a.Hk + h) * D + e0) = p;
+    if (a.slots) store(p, h, live, a.cache.k_ts, a.cache.k_codes, a.cache.k_scales);
+  });
+
+  // ---- values
+  if (a.Hv) each_row<2>(a.v + tok * a.v_stride, a.Hv, first(nk), sub, step, D, e0, [&](const uint4& p, int h, bool live) {
+    store(p, h, live, a.cache.v_ts, a.cache.v_codes, a.cache.v_scales);
+  });
+
+  // ---- queries, in float32, two elements an instruction
+  if (a.Hq) each_row<4>(a.q + tok * a.q_stride, a.Hq, first(nk + nv), sub, step, D, e0, [&](const uint4& p, int h, bool live) {
+    uint64_t y[4];
+    unpack8x2(p, y);
+    float rs = 1.0f;
+    double far_rs = 0.0;
+    if (a.q_weight) {
+      uint64_t s2 = mul2(y[0], y[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(y[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    if (!live) continue;
-    const int slot = a.slots[t0 + t];
-    if (slot < 0 || slot >= n_slots) {
-      if (slot >= 0) atomicExch(a.status, kStatusInvalid);
-      continue;
+      for (int i = 1; i < 4; ++i) s2 = fma2(y[i], y[i], s2);
+      float sa, sb;
+      unpack2(s2, sa, sb);
+      float ss = sa + sb;
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      rs = rsqrtf(ss * (1.0f / D) + (float)a.eps);
+      const bool far = !(ss < 1e36f && ss > 1e-30f) && live;  // squares near the ends of float32's range
+      if (__any_sync(0xffffffffu, far)) {
+        double sd = 0.0;
+        float v[8];
+        unpack8(p, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sd = fma((double)v[i], (double)v[i], sd);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+        if (far) {
+          far_rs = norm_factor(sd, D, a.eps);
+          rs = 1.0f;
+        }
+      }
     }
-    const float* tsp = kind == 1 ? a.cache.k_ts : a.cache.v_ts;
-    uint32_t c;
-    const uint32_t s = quantize_half16(y, sign_bits(p), amax, tsp ? tsp[h] : 1.0f, &c);
-    const int page = slot >> a.page_shift, off = slot & (a.cache.page_size - 1);
-    const int64_t row = ((int64_t)page * a.cache.Hkv + h) * a.cache.page_size + off;
-    uint8_t* codes = kind == 1 ? a.cache.k_codes : a.cache.v_codes;
-    uint8_t* scales = kind == 1 ? a.cache.k_scales : a.cache.v_scales;
-    *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + e0 / 2) = c;
-    if ((lane & 1) == 0) scales[row * (D / 16) + e0 / 16] = (uint8_t)s;
-  }
+    const uint4 pp = hop ? partner(p) : beside(p);
+    uint64_t q[4];
+    unpack8x2(pp, q);
+    if (far_rs != 0.0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float u, v;
+        unpack2(y[i], u, v);
+        y[i] = pack2((float)(u * far_rs), (float)(v * far_rs));
+        unpack2(q[i], u, v);
+        q[i] = pack2((float)(u * far_rs), (float)(v * far_rs));
+      }
+    }
+    const uint64_t* ta = reinterpret_cast<const uint64_t*>(s_qa[t]) + lane;
+    const uint64_t* tb = reinterpret_cast<const uint64_t*>(s_qb[t]) + lane;
+    const uint64_t r2 = pack2(rs, rs);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = mul2(y[i], ta[i * L]);
+      if (turned) y[i] = fma2(q[i], tb[i * L], y[i]);
+      float lo, hi;
+      unpack2(mul2(y[i], r2), lo, hi);
+      o[i] = pack_bf16(lo, hi);
+    }
+    if (live)
+      *reinterpret_cast<uint4*>(a.q_out + ((int64_t)tok * a.Hq + h) * D + e0) = make_uint4(o[0], o[1], o[2], o[3]);
+  });
 }
 
 // 8 elements a thread and output: 4 bytes of codes and the block's scale -> one 16-byte store
@@ -357,9 +443,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int p
 }  // namespace
 
 cudaError_t launch_qkv_prep(const QkvPrepArgs& a, int D, int num_sms, cudaStream_t st) {
-  // few tokens: a block each, so that all of them run at once
-  const int tokens = a.T > 8 * num_sms ? kPrepTokens : 1;
-  const dim3 grid((a.T + tokens - 1) / tokens), block(kPrepThreads);
+  const int tokens = a.T > 4 * num_sms ? kManyWarps : 1;
+  const dim3 grid((a.T + tokens - 1) / tokens), block(32 * (tokens > 1 ? kManyWarps : kFewWarps));
   if (D == 64) return launch_pdl(qkv_prep_kernel<64>, grid, block, 0, st, a, tokens);
   if (D == 128) return launch_pdl(qkv_prep_kernel<128>, grid, block, 0, st, a, tokens);
   return launch_pdl(qkv_prep_kernel<256>, grid, block, 0, st, a, tokens);
