@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
   __shared__ uint64_t s_full[W][kStages];
   __shared__ uint32_t s_bad[W][kStages];  // 16-key halves whose page number is outside the cache
   __shared__ float s_m[W][RB], s_l[W][RB];
+  __shared__ __align__(16) uint4 s_q[RB * D / 8];
+  __shared__ int s_e[RB];
   __shared__ float s_mm[RB], s_ll[RB];
   __shared__ long long s_scan[W];
   __shared__ long long s_local;
@@ -286,49 +288,54 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
   while (more) {
     if (!filled) prime(it);  // (the page number comes beside the queries)
     const int tok_end = tok_end_of(it), rows = it.sq.n_q * a.G, row_first = it.row_first, h = it.h;
-    // ---- queries: thread (g, c) holds row g's quarter c as the B operand of every k step
-    uint4 raw[NR][D / 32];
+    // ---- queries: converted once by the block, 8 elements a thread, into shared memory; then thread
+    // (g, c) holds row g's quarter c as the B operand of every k step. (Every warp converting for
+    // itself was 300 instructions of code that runs once: its fetches took 4 us at D = 256.)
+    constexpr int QL = D / 8;  // threads of a row; a quarter's 16-byte pieces are turned about by
+                               // row and quarter, so that 8 lanes read 8 different places
+    auto turned = [](int row, int qtr, int piece) {
+      const int x = D == 256 ? ((row & 1) << 2) | qtr : D == 128 ? ((row & 1) << 1) | (qtr >> 1) : row & 1;
+      return row * (D / 8) + qtr * (D / 32) + (piece ^ x);
+    };
+#pragma unroll 1
+    for (int i = tid; i < (RB * QL + 31) / 32 * 32; i += THREADS) {
+      const int r = i / QL, piece = i % QL, row = row_first + r;
+      const bool live = row < rows && r < RB;
+      const int tok = live ? row / a.G : 0, head = h * a.G + (live ? row - tok * a.G : 0);
+      const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(it.sq.q0 + tok) * a.q_stride + (int64_t)head * D) + piece)
+                             : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t m2 = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu), __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
+      int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7) - 127;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int row = row_first + 8 * r + g;
-      const bool ok = row < rows;
-      const int tok = ok ? row / a.G : 0, head = h * a.G + (ok ? row - tok * a.G : 0);
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(it.sq.q0 + tok) * a.q_stride + (int64_t)head * D +
-                                                        c * (D / 4));
+      for (int d = QL / 2; d > 0; d >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, d));
+      e = max(e, -100);
+      const float up = __int_as_float((127 + 13 - e) << 23);  // the row's largest element becomes 2^13..2^14
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      uint32_t f[4];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) raw[r][i] = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < 4; ++j) f[j] = pack_f16(bf16_to_f32(w[j] & 0xFFFFu) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
+      s_q[turned(r, piece / (D / 32), piece % (D / 32))] = make_uint4(f[0], f[1], f[2], f[3]);
+      if (piece == 0) s_e[r] = e;
     }
     if (!filled) fill(it);
+    __syncthreads();
     uint32_t bq[NR][KSTEPS][2];
     float fac[NR][2];
     int lim[NR][2], lim_min = 0x7fffffff;
     const float kts = a.cache.k_ts ? a.cache.k_ts[h] : 1.0f;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        mx = __vmaxu2(mx, raw[r][i].x & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, raw[r][i].y & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, raw[r][i].z & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, raw[r][i].w & 0x7FFF7FFFu);
-      }
-      int e = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-      e = max(e, -100);
-      const float up = __int_as_float((127 + 13 - e) << 23);  // the row's largest element becomes 2^13..2^14
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t w[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          bq[r][2 * i + (j >> 1)][j & 1] =
-              pack_f16(bf16_to_f32(w[j] & 0xFFFFu) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
+        const uint4 f = s_q[turned(8 * r + g, c, i)];
+        bq[r][2 * i][0] = f.x;
+        bq[r][2 * i][1] = f.y;
+        bq[r][2 * i + 1][0] = f.z;
+        bq[r][2 * i + 1][1] = f.w;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int ej = __shfl_sync(0xffffffffu, e, 4 * (2 * c + j));
+        const int ej = s_e[8 * r + 2 * c + j];
         fac[r][j] = a.scale * kLog2e * kts * __int_as_float((127 - 13 + ej) << 23);
         const int rj = row_first + 8 * r + 2 * c + j;
         // keys that row may see: all of the context, or up to its own position
@@ -356,8 +363,17 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
       const uint32_t slot = n_used % kStages;
       if (!__all_sync(0xffffffffu, wait_soon(&s_full[warp][slot], (n_used / kStages) & 1, &s_wait, a.status))) break;
       ++n_used;
-      const uint8_t* st = ring + slot * stage_bytes(D);
+      uint8_t* st = ring + slot * stage_bytes(D);
       const uint32_t bad = s_bad[warp][slot];
+      if (bad || t_stage + kStageKeys > it.sq.ctx) {
+        // keys past the end, whatever the page holds there, and rows of no page count as zeros
+        for (int i = lane; i < kStageKeys * (D / 16); i += 32) {
+          const int r = i / (D / 16);
+          if (((bad >> (r / 16)) & 1u) || t_stage + r >= it.sq.ctx) st[kKs + i] = st[kVs + i] = 0;
+        }
+        fence_proxy_async_smem();  // (before the next copy over them)
+        __syncwarp();
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t0 = t_stage + 16 * half;
@@ -375,7 +391,6 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
           load_words<VW>(vv[i], vc + i * 4 * (D / 2));
           vs[i] = load_scales<VS>(st + kVs + (16 * half + c + 4 * i) * (D / 16) + (D >= 128 ? g * VS : g / 2));
         }
-        if ((bad >> half) & 1u) ks[0] = ks[1] = vs[0] = vs[1] = vs[2] = vs[3] = 0u;  // rows of no page count as zeros
         // S^T = K Q^T
         float s[NR][4];
 #pragma unroll
@@ -440,11 +455,6 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
           pb[r][1] = transpose8x8(pack_f16(p[2], p[3]));
         }
         // O^T += V^T P^T
-        if (t0 + 16 > it.sq.ctx) {  // keys past the end: whatever the page holds there counts as 0
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (t0 + c + 4 * i >= it.sq.ctx) vs[i] = 0;
-        }
         const uint32_t va = __byte_perm(vs[0], vs[1], 0x5140), vb = __byte_perm(vs[2], vs[3], 0x5140);
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
