@@ -1,21 +1,29 @@
 // Attention of many query rows per key head over the paged NVFP4 cache (prompts and chunks of
 // prompts): out = softmax(scale q K^T) V, both products on the tcgen05 tensor cores.
 //
-// A block takes tiles of 128 query rows of one key head (row = token * G + head of the group, so
-// the G heads that share keys share the expanded keys too) and walks over the keys KT at a time (128; 64 for D = 256, whose
-// O and Q leave TMEM no room for more):
+// A block takes tiles of query rows of one key head (row = token * G + head of the group, so the
+// G heads that share keys share the expanded keys too), 256 rows for D <= 128 and 128 for D = 256,
+// and walks over the keys KT at a time:
 //   loader warp: a tile's codes and scales by bulk copies (a page's rows of one head are
-//     contiguous) into a ring of raw slots, several ahead.
+//     contiguous) into a ring of raw slots, some ahead.
 //   expander warps: raw slots to float16 (exact: 2 + 4 significant bits) in the 128-byte
 //     swizzle. K rows are the K-major B operand of S = Q K^T; V rows, stored the same way, are
 //     the MN-major B operand of O += P V, so neither is transposed.
-//   MMA warp: S = Q K^T, then O += P V of the tile before. Q (float16, scaled by a power of two
-//     per row) and P are A operands in TMEM: a product with two operands in shared memory reads
-//     it at its full rate, beside the writes of the expanded tiles.
-//   softmax warps: two threads a row, each half of the keys. They copy S to registers first, so
-//     the next Q K^T can overwrite it while they work, and a tile's softmax has a PV and a QK of
-//     time. O is rescaled only when a row's maximum rises by more than 2^8 over the one in use;
+//   two MMA warps: S = Q K^T, and O += P V. Q is float16, scaled by a power of two per row; P, an
+//     A operand in TMEM, float16 too.
+//   softmax warps: they copy S to registers first, so the next Q K^T can overwrite it while they
+//     work. O is rescaled only when a row's maximum rises by more than 2^8 over the one in use;
 //     the weights are below 2^8 in float16, the sums in float32.
+// D <= 128: two groups of 128 rows, a softmax thread to a row, KT = 128. The groups share the
+//   expanded keys, which are a third of a softmax's instructions again, and S; O of both, S and
+//   both P fill TMEM, so Q is in shared memory. Bound by the softmax warps' instructions and the
+//   exponentials (256 x 128 scores in 3400 cycles, the products alone 2450). One group of 128 rows
+//   a block with two threads a row took 2430 cycles for half as many: 27140 tokens in chunks over
+//   caches up to 16K (32 + 8 heads, D = 128) 3350 us, now 2400 us.
+// D = 256: O, Q and S of 128 rows leave no columns for a second group or more than KT = 64 keys,
+//   at which a Q K^T costs as much as at 128; bound by the products (1536 cycles of 1750 a tile).
+// The loops are kept short where that costs nothing: the roles' code together passes the
+// instruction cache (an expander unrolled 16 times instead of 4 made the softmax 12% slower).
 //
 // Tiles have different numbers of keys (causal, ragged), so the work (key tiles, plus a few for
 // each row tile's start and end) is dealt to the blocks in equal contiguous runs; a plan kernel
@@ -29,25 +37,50 @@ namespace moe {
 
 namespace {
 
-constexpr int kRows = 128;
-constexpr int kSoftWarps = 8, kExpWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kExpWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kTcThreads = 32 * (kSoftWarps + kExpWarps + 4);  // five whole warpgroups
-// Registers of a thread: at the launch (what 640 threads may have), then by role. A role's
-// setmaxnreg waits for registers that others gave back, so the shares must not exceed the launch's.
-constexpr int kLaunchRegs = 96, kSoftRegs = 144, kExpRegs = 64, kLastRegs = 64;
-static_assert(32 * (kSoftWarps * kSoftRegs + kExpWarps * kExpRegs + 4 * kLastRegs) <= kTcThreads * kLaunchRegs, "registers");
-
+constexpr int kHalf = 128;  // rows of one M = 128 product
+constexpr int kSoftWarps = 8;
 constexpr int kPlanThreads = 1024;
-// A row tile's start and end (its queries in, its rows out), in key tiles: 10000 cycles of 2500
-// at D = 128, 19000 of 1900 at D = 256.
-__host__ __device__ constexpr int start_cost(int D) { return D == 256 ? 10 : 5; }
 
-__host__ __device__ constexpr int key_tile(int D) { return D == 256 ? 64 : 128; }
-constexpr int kTcStages = 2;  // expanded tiles of K, and of V
-constexpr int kRawSlots = 8;  // raw tiles, K and V in turn
-__host__ __device__ constexpr int raw_bytes(int D) { return key_tile(D) * (D / 2 + D / 16); }
-constexpr int tc_smem(int D) { return 2 * kTcStages * key_tile(D) * D * 2 + kRawSlots * raw_bytes(D) + 1024; }
+// The two forms. `pair`: two threads share a row of scores and a tile has 128 rows; otherwise a
+// thread has a row, and a tile 256 rows, half of them to each group of four softmax warps.
+template <int D>
+struct Tc {
+  static constexpr bool pair = D == 256;
+  static constexpr int rows = pair ? kHalf : 2 * kHalf;  // of a tile
+  static constexpr int kt = pair ? 64 : 128;             // keys of a tile
+  static constexpr int exp_warps = pair ? 8 : 4;         // expanders, half of them for K
+  static constexpr int mma_warp = kSoftWarps + exp_warps, load_warp = mma_warp + 2;
+  static constexpr int threads = 32 * (kSoftWarps + exp_warps + 4);  // whole warpgroups
+  // Registers of a thread: at the launch (what so many threads may have), then by role. A role's
+  // setmaxnreg waits for registers that others gave back, so the shares must not exceed the
+  // launch's.
+  static constexpr int launch_regs = pair ? 96 : 128, soft_regs = pair ? 144 : 184;
+  static constexpr int exp_regs = pair ? 64 : 72, last_regs = pair ? 64 : 72;
+  static_assert(32 * (kSoftWarps * soft_regs + exp_warps * exp_regs + 4 * last_regs) <= threads * launch_regs, "registers");
+  // TMEM columns: O, Q, S, two P; or the groups' O, S, and the groups' P
+  static constexpr uint32_t q_col = D, s_col = pair ? q_col + D / 2 : 2 * D, p_col = s_col + kt;
+  static_assert(p_col + kt <= 512, "TMEM columns");
+  static constexpr int stages = 2;                       // expanded tiles of K, and of V
+  static constexpr int raw_slots = D == 128 ? 3 : 8;     // raw tiles, K and V in turn
+  static constexpr int tile_bytes = kt * D * 2;
+  static constexpr int raw_bytes = kt * (D / 2 + D / 16);
+  static constexpr int q_bytes = pair ? 0 : rows * D * 2;
+  static constexpr int smem = q_bytes + 2 * stages * tile_bytes + raw_slots * raw_bytes + 1024;
+  // A row tile's start and end (its queries in, its rows out), in key tiles: 14500 cycles of 3400
+  // at D = 128, 19000 of 1800 at D = 256.
+  static constexpr int start_cost = pair ? 10 : 4;
+};
+
+struct TcShared {
+  uint64_t raw_full[8], raw_empty[8], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2], s_empty, p_full[2], pv_done[2], drained[2];
+  uint32_t bad[8];  // of a raw slot: groups of 16 keys whose page number is outside the cache
+  uint32_t tmem;
+  int idx;
+  Patience wait;
+  float x[2][kHalf];
+  int e[2][kHalf];
+};
 
 // Row tiles of one key head, in order; a tile's share of the work starts at `start`.
 struct RowTile {
@@ -57,15 +90,15 @@ struct RowTile {
 };
 
 // keys that the tile's last row sees
-MOE_DEV int tile_keys(const KvAttnArgs& a, const SeqSpan& s, int tile) {
+MOE_DEV int tile_keys(const KvAttnArgs& a, const SeqSpan& s, int tile, int tile_rows) {
   if (!a.causal) return s.ctx;
-  const int last = min(s.n_q * a.G, (tile + 1) * kRows) - 1;
+  const int last = min(s.n_q * a.G, (tile + 1) * tile_rows) - 1;
   return min(s.ctx, max(s.ctx - s.n_q + last / a.G + 1, 0));
 }
 
-MOE_DEV int seq_tiles(const KvAttnArgs& a, const SeqSpan& s) {
+MOE_DEV int seq_tiles(const KvAttnArgs& a, const SeqSpan& s, int tile_rows) {
   const int rows = s.n_q * a.G;
-  return rows > a.dec_max_rows ? (rows + kRows - 1) / kRows : 0;
+  return rows > a.dec_max_rows ? (rows + tile_rows - 1) / tile_rows : 0;
 }
 
 // Exclusive block scan of one value per thread (kPlanThreads threads); *total the sum.
@@ -95,7 +128,7 @@ MOE_DEV long long plan_scan(long long v, long long* tmp, long long* total) {
 }
 
 // One block: the list of row tiles and the prefix sums of their work.
-__global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttnArgs a, int kt, int start_cost) {
+__global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttnArgs a, int tile_rows, int kt, int start_cost) {
   MOE_PDL_PROLOGUE();
   __shared__ long long tmp[32];
   RowTile* tiles = reinterpret_cast<RowTile*>(a.tiles);
@@ -103,7 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttn
   long long at = 0;
   for (int b0 = 0; b0 < a.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    const int n = b < a.n_seqs ? seq_tiles(a, load_seq(a, b)) : 0;
+    const int n = b < a.n_seqs ? seq_tiles(a, load_seq(a, b), tile_rows) : 0;
     long long sum;
     const long long first = at + plan_scan(n, tmp, &sum);
     for (int i = 0; i < n && first + i < a.max_tiles; ++i) {
@@ -123,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttn
     int units = 0;
     if (i < n_tiles) {
       const SeqSpan s = load_seq(a, tiles[i].b);
-      units = max(1, (tile_keys(a, s, tiles[i].tile) + kt - 1) / kt);
+      units = max(1, (tile_keys(a, s, tiles[i].tile, tile_rows) + kt - 1) / kt);
     }
     long long sum;
     const long long start = at + plan_scan(i < n_tiles ? units + start_cost : 0, tmp, &sum);
@@ -172,6 +205,16 @@ MOE_DEV void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint3
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] x B[smem]^T, float16 -> float32, K = 16
+MOE_DEV void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Instruction descriptor, float16 A and B, float32 accumulator; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -212,6 +255,13 @@ MOE_DEV bool bar_or(int id, int n, bool p) {
       : "r"(id), "r"(n), "r"((uint32_t)p)
       : "memory");
   return r != 0;
+}
+
+// the largest of three
+MOE_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // 2^x for a pair, without the special-function unit: x = n + f with n whole and |f| <= 1/2, a
@@ -281,57 +331,681 @@ struct Walk {
   }
 };
 
+
+// ---------------------------------------------------------------- softmax, two threads a row
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
-  constexpr int KT = key_tile(D), HK = KT / 2, NS = kTcStages, RAW = kRawSlots;
-  constexpr int EW = kExpWarps / 2;  // expander warps of K, and of V
-  constexpr uint32_t kTileBytes = KT * D * 2;
-  // TMEM columns: O, Q, S, two P
-  constexpr uint32_t kO = 0, kQ = D, kS = kQ + D / 2, kP = kS + KT;
-  static_assert(kP + KT <= 512, "TMEM columns");
+MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_t tmem, long long total, int grid) {
+  using C = Tc<D>;
+  constexpr int KT = C::kt, HK = KT / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 2, quarter = warp & 3;  // half of the keys, of Q and of O
+  const int row = quarter * 32 + lane;
+  const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+  uint32_t tc = 0;  // key tiles so far
+  bool ok = true;
+  Run run;
+  while (ok && walk.next(&run)) {
+    const SeqSpan sq = load_seq(a, run.b);
+    const int rows = sq.n_q * a.G, rr = run.tile * kHalf + row;
+    const bool live = rr < rows;
+    const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
+    const float ks = a.scale * (a.cache.k_ts ? a.cache.k_ts[run.h] : 1.0f) * kLog2e;
+    // ---- Q: this thread's half of the row
+    float fac;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride +
+                                                        (int64_t)head * D + half * (D / 2));
+      uint4 raw[D / 16];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[i].w & 0x7FFF7FFFu);
+      }
+      sh.e[half][row] = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;
+      named_bar_sync(5, kSoftWarps * 32);
+      const int e = max(max(sh.e[0][row], sh.e[1][row]), -100);
+      // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
+      const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
+      fac = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        uint32_t f[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w[4] = {raw[4 * i + j].x, raw[4 * i + j].y, raw[4 * i + j].z, raw[4 * i + j].w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            f[4 * j + u] = pack_f16(bf16_to_f32(w[u] & 0xFFFFu) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
+        }
+        tmem_st16(tl + C::q_col + half * (D / 4) + 16 * i, f);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[0]);
+    }
+    const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
+    // keys that every row of the tile sees
+    const int first_tok = run.tile * kHalf / a.G;
+    const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
+    float m = kNoMax;
+    uint64_t l2 = pack2(0.0f, 0.0f);
+    const uint64_t fac2 = pack2(fac, fac);
+    for (int u = run.u0; u < run.u1; ++u, ++tc) {
+      // the scores, and the product that last read this tile's columns of P
+      if (tc >= 2)
+        ok = wait_both(&sh.s_full[0], tc & 1, &sh.pv_done[tc & 1], ((tc >> 1) - 1) & 1, &sh.wait, a.status) && ok;
+      else
+        ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[0], tc & 1, &sh.wait, a.status)) && ok;
+      tc_fence_after();
+      uint32_t s[HK];
+#pragma unroll
+      for (int i = 0; i < HK; i += 32) tmem_ld32(tl + C::s_col + half * HK + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_empty);
+      if (u * KT + KT > lim_min) {
+        const int left = lim - u * KT - half * HK;
+#pragma unroll
+        for (int i = 0; i < HK; ++i)
+          if (i >= left) s[i] = 0xff800000u;
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < HK; i += 2)
+        mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
+      // the two warps of these 32 rows decide together
+      if (bar_or(1 + quarter, 64, mx > m + kRaise || !ok)) {
+        sh.x[half][row] = mx;
+        if (bar_or(1 + quarter, 64, !ok)) {
+          ok = false;
+          break;
+        }
+        const float top = fmaxf(fmaxf(sh.x[0][row], sh.x[1][row]), m);
+        if (u > run.u0) {
+          const float fix = ex2(m - top);
+          float a0, a1;
+          unpack2(l2, a0, a1);
+          l2 = pack2(a0 * fix, a1 * fix);
+          ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &sh.wait, a.status));
+          tc_fence_after();
+          if (ok) {
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tl + half * (D / 2) + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+              tmem_st32(tl + half * (D / 2) + c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        m = top;
+        bar_or(1 + quarter, 64, false);  // s_x is free again
+      }
+      const uint64_t nm2 = pack2(-m, -m);
+      const uint32_t tp = tl + C::p_col + (tc & 1) * (KT / 2) + half * (HK / 2);
+#pragma unroll
+      for (int q = 0; q < HK / 32; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
+          float x0, x1;
+          if (D < 256 && i % 4 == 3) {  // a quarter of them past the special-function unit, the busiest one here
+            ex2_pair(x, x0, x1);
+          } else {
+            unpack2(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+          }
+          l2 = add2(l2, pack2(x0, x1));
+          p[i] = pack_f16(x0, x1);
+        }
+        tmem_st16(tp + 16 * q, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[tc & 1]);
+    }
+    // ---- the run's result
+    float l0, l1;
+    unpack2(l2, l0, l1);
+    sh.x[half][row] = l0 + l1;
+    if (ok) ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &sh.wait, a.status));
+    tc_fence_after();
+    if (bar_or(5, kSoftWarps * 32, !ok)) break;
+    const float ll = sh.x[0][row] + sh.x[1][row];
+    const bool whole = run.u0 == 0 && run.u1 == run.n_units;
+    const float vts = a.cache.v_ts ? a.cache.v_ts[run.h] : 1.0f;
+    const float f = !whole ? 1.0f : ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
+    const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
+    const int side = run.u0 > 0 ? 0 : 1;
+    float* part = a.partial + ((size_t)blockIdx.x * 2 + side) * a.part_stride;
+#pragma unroll
+    for (int c = 0; c < D / 2; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(tl + half * (D / 2) + c, o);
+      tmem_ld_wait();
+      if (whole) {
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + half * (D / 2) + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * j]) * f,
+                                                             __uint_as_float(o[8 * i + 2 * j + 1]) * f);
+              w[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(part + 2 * kHalf + row * D + half * (D / 2) + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                               __uint_as_float(o[4 * i + 3]));
+      }
+    }
+    if (half == 0) {
+      if (!whole) {
+        part[row] = m;
+        part[kHalf + row] = ll;
+      } else if (live && a.lse) {
+        a.lse[out_row] = ll == 0.0f ? -INFINITY : (m + log2f(ll)) * kLn2;
+      }
+    }
+    if (!whole && side == 1 && threadIdx.x == 0) {
+      int last = blockIdx.x + 1;
+      while (total * (last + 1) / grid < run.end) ++last;
+      a.meta[blockIdx.x] = make_int4(run.b, run.h, run.tile * kHalf, last);
+    }
+    tc_fence_before();
+    named_bar_sync(5, kSoftWarps * 32);  // s_x and s_e are free again, O has been read
+  }
+}
+
+// ---------------------------------------------------------------- softmax, a thread a row
+// Group g of four warps has the rows g * 128.. of the tile, and its own O and P in TMEM; group 1
+// passes over a tile of no more than 128 rows. Both use one S: a group copies its scores to
+// registers first, and the other group's Q K^T follows into the same columns, so the groups work
+// half a period apart and neither waits for its own products.
+template <int D>
+MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_t tmem, uint8_t* s_q, long long total,
+                          int grid) {
+  using C = Tc<D>;
+  constexpr int KT = C::kt;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = warp >> 2, quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16), to = tl + g * D, tp = tl + C::p_col + g * (KT / 2);
+  uint32_t tc = 0;  // key tiles of this group so far
+  bool ok = true;
+  Run run;
+  while (ok && walk.next(&run)) {
+    const SeqSpan sq = load_seq(a, run.b);
+    const int rows = sq.n_q * a.G, n = run.u1 - run.u0, first_row = run.tile * C::rows + g * kHalf;
+    if (g == 1 && rows - run.tile * C::rows <= kHalf) continue;
+    const int rr = first_row + row;
+    const bool live = rr < rows;
+    const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
+    float m = kNoMax;
+    uint64_t l2 = pack2(0.0f, 0.0f);
+    float fac;
+    const float ks = a.scale * (a.cache.k_ts ? a.cache.k_ts[run.h] : 1.0f) * kLog2e;
+    // ---- Q, float16 scaled by a power of two, K-major in the 128-byte swizzle
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride + (int64_t)head * D);
+      uint4 raw[D / 8];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, raw[i].w & 0x7FFF7FFFu);
+      }
+      const int e = max((int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127, -100);
+      // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
+      const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
+      fac = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
+      uint8_t* dst = s_q + g * (kHalf * D * 2) + row * 128;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          f[u] = pack_f16(bf16_to_f32(w[u] & 0xFFFFu) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
+        *reinterpret_cast<uint4*>(dst + (i / 8) * (kHalf * 128) + (((i % 8) ^ (row & 7)) << 4)) =
+            make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();  // O of the run before has been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[g]);
+    }
+    const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
+    // keys that every row of this half sees
+    const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_row / a.G + 1, 0) : sq.ctx;
+    const uint64_t fac2 = pack2(fac, fac);
+    for (int j = 0; j < n; ++j, ++tc) {
+      ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[g], tc & 1, &sh.wait, a.status));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[KT];
+#pragma unroll
+      for (int i = 0; i < KT; i += 32) tmem_ld32(tl + C::s_col + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_empty);
+      const int k0 = (run.u0 + j) * KT;
+      if (k0 + KT > lim_min) {
+        const int left = lim - k0;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+          if (i >= left) s[i] = 0xff800000u;
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < KT; i += 2)
+        mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
+      if (__any_sync(0xffffffffu, mx > m + kRaise)) {
+        const float top = fmaxf(mx, m);
+        if (j > 0) {
+          const float fix = ex2(m - top);
+          float a0, a1;
+          unpack2(l2, a0, a1);
+          l2 = pack2(a0 * fix, a1 * fix);
+          ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+            tmem_st16(to + c, o);
+          }
+          tmem_st_wait();
+        }
+        m = top;
+      }
+      const uint64_t nm2 = pack2(-m, -m);
+#pragma unroll
+      for (int q = 0; q < KT / 32; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
+          float x0, x1;
+          if (i % 4 == 3) {  // a quarter of them past the special-function unit, the busiest one here
+            ex2_pair(x, x0, x1);
+          } else {
+            unpack2(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+          }
+          l2 = add2(l2, pack2(x0, x1));
+          p[i] = pack_f16(x0, x1);
+        }
+        if (q == 0 && tc > 0) {  // the product that last read these columns
+          ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
+          tc_fence_after();
+        }
+        tmem_st16(tp + 16 * q, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&sh.p_full[g]);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
+    if (!ok) break;
+    tc_fence_after();
+    // ---- the run's result
+    float l0, l1;
+    unpack2(l2, l0, l1);
+    const float ll = l0 + l1;
+    const bool whole = run.u0 == 0 && run.u1 == run.n_units;
+    const float vts = a.cache.v_ts ? a.cache.v_ts[run.h] : 1.0f;
+    const float f = !whole ? 1.0f : ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
+    const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
+    const int side = run.u0 > 0 ? 0 : 1;
+    float* part = a.partial + ((size_t)blockIdx.x * 2 + side) * a.part_stride;
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(to + c, o);
+      tmem_ld_wait();
+      if (whole) {
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * j]) * f,
+                                                             __uint_as_float(o[8 * i + 2 * j + 1]) * f);
+              w[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(part + 2 * C::rows + (g * kHalf + row) * D + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                               __uint_as_float(o[4 * i + 3]));
+      }
+    }
+    if (!whole) {
+      part[g * kHalf + row] = m;
+      part[C::rows + g * kHalf + row] = ll;
+    } else if (live && a.lse) {
+      a.lse[out_row] = ll == 0.0f ? -INFINITY : (m + log2f(ll)) * kLn2;
+    }
+    if (!whole && side == 1 && threadIdx.x == 0) {
+      int last = blockIdx.x + 1;
+      while (total * (last + 1) / grid < run.end) ++last;
+      a.meta[blockIdx.x] = make_int4(run.b, run.h, run.tile * C::rows, last);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- expanders
+// 16 elements (8 bytes of codes, one scale) a lane and step, lanes side by side in the raw
+// slot. A step is a whole number of 8 rows on, so a lane keeps its place in the swizzle; of its
+// two 16-byte stores, lanes that would meet in a bank take the second one first.
+template <int D>
+MOE_DEV void expand(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_k, uint8_t* s_v, uint8_t* s_raw) {
+  constexpr int KT = Tc<D>::kt, NS = Tc<D>::stages, RAW = Tc<D>::raw_slots;
+  constexpr int EW = Tc<D>::exp_warps / 2;  // expander warps of K, and of V
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int P = D / 16;                 // lanes of a row
+  constexpr int STEPS = KT * P / (32 * EW), ROWS = 32 / P * EW;  // rows of a step
+  constexpr int BATCH = STEPS < 4 ? STEPS : 4;  // loads before the first use
+  static_assert(ROWS % 8 == 0 && STEPS % BATCH == 0, "a lane keeps its row modulo 8");
+  const int pw = (warp - kSoftWarps) % EW;
+  const bool is_v = warp >= kSoftWarps + EW;
+  uint64_t* full = is_v ? sh.v_full : sh.k_full;
+  uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
+  const int row0 = (pw * 32 + lane) / P, part = lane % P;
+  const bool swap = D >= 128 && (part & 4);
+  const uint32_t off0 = (part >> 2) * (KT * 128) + row0 * 128 + (((((part & 3) << 1) | (swap ? 1 : 0)) ^ (row0 & 7)) << 4);
+  const uint32_t off1 = off0 ^ 16;
+  uint32_t tc = 0;
+  bool ok = true;
+  Run run;
+  while (ok && walk.next(&run)) {
+    const int ctx = load_seq(a, run.b).ctx;
+#pragma unroll 1
+    for (int u = run.u0; u < run.u1; ++u, ++tc) {
+      const uint32_t n_raw = 2 * tc + (is_v ? 1 : 0), slot = n_raw % RAW, s = tc % NS;
+      ok = wait_both(&sh.raw_full[slot], (n_raw / RAW) & 1, &empty[s], ((tc / NS) & 1) ^ 1, &sh.wait, a.status);
+      if (!ok) break;
+      const uint8_t* raw = s_raw + slot * Tc<D>::raw_bytes;
+      const uint32_t bad = sh.bad[slot];
+      const int left = ctx - u * KT;
+      uint8_t* dst = (is_v ? s_v : s_k) + s * Tc<D>::tile_bytes;
+#pragma unroll 1
+      for (int first = 0; first < STEPS; first += BATCH) {
+        uint2 codes[BATCH];
+        uint32_t scales[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          codes[i] = reinterpret_cast<const uint2*>(raw)[((first + i) * EW + pw) * 32 + lane];
+          scales[i] = (raw + KT * (D / 2))[((first + i) * EW + pw) * 32 + lane];
+        }
+        if (bad || left < KT) {  // keys past the end, and pages outside the cache, count as zeros
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int row = row0 + (first + i) * ROWS;
+            if (row >= left || ((bad >> (row / 16)) & 1u)) scales[i] = 0u;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const uint32_t w0 = swap ? codes[i].y : codes[i].x, w1 = swap ? codes[i].x : codes[i].y;
+          const uint32_t sc = e4m3x2_to_f16x2(scales[i] * 0x0101u);
+          uint32_t f[4];
+          e2m1x8_to_f16x2x4(w0, f);
+          *reinterpret_cast<uint4*>(dst + off0 + (first + i) * (ROWS * 128)) =
+              make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+          e2m1x8_to_f16x2x4(w1, f);
+          *reinterpret_cast<uint4*>(dst + off1 + (first + i) * (ROWS * 128)) =
+              make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.raw_empty[slot]);
+        mbar_arrive(&full[s]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- loader
+template <int D>
+MOE_DEV void load_raw(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_raw) {
+  constexpr int KT = Tc<D>::kt, RAW = Tc<D>::raw_slots;
+  const int lane = threadIdx.x & 31;
+  // a lane copies one page's part of the tile: at most KT / 16 pages
+  uint32_t n_raw = 0;
+  bool ok = true;
+  Run run;
+  const int ps = a.cache.page_size;
+  const int rows = min(ps, KT);               // of a copy
+  const int copies = KT / rows;               // of a slot
+  while (ok && walk.next(&run)) {
+    const int ctx = load_seq(a, run.b).ctx;
+    const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
+    auto page_of = [&](int u) {
+      const int t = u * KT + lane * rows;
+      return lane < copies && t < ctx ? __ldg(table + (t >> a.page_shift)) : 0;
+    };
+    int page = page_of(run.u0);
+    for (int u = run.u0; u < run.u1 && ok; ++u) {
+      const int next = page_of(u + 1);
+      const int t = u * KT + lane * rows;
+      const bool wanted = lane < copies && t < ctx;
+      const bool good = wanted && page >= 0 && page < a.cache.n_pages;
+      if (wanted && !good) atomicExch(a.status, kStatusInvalid);
+      const uint32_t bads = __ballot_sync(0xffffffffu, wanted && !good), goods = __ballot_sync(0xffffffffu, good);
+      const int64_t row = ((int64_t)page * a.cache.Hkv + run.h) * ps + (t & (ps - 1));
+      uint32_t bad = 0;  // a copy of `rows` keys is rows / 16 groups of 16
+      for (int j = 0; bads && j < copies; ++j)
+        if ((bads >> j) & 1u) bad |= ((1u << (rows / 16)) - 1u) << (j * (rows / 16));
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i, ++n_raw) {  // K, then V
+        const uint32_t slot = n_raw % RAW;
+        ok = __all_sync(0xffffffffu, wait_soon(&sh.raw_empty[slot], ((n_raw / RAW) & 1) ^ 1, &sh.wait, a.status));
+        if (!ok) break;
+        uint8_t* raw = s_raw + slot * Tc<D>::raw_bytes;
+        if (lane == 0) {
+          sh.bad[slot] = bad;
+          mbar_arrive_expect_tx(&sh.raw_full[slot], __popc(goods) * rows * (D / 2 + D / 16));
+        }
+        __syncwarp();
+        if (good) {
+          bulk_g2s(raw + lane * rows * (D / 2), (i ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2), rows * (D / 2),
+                   &sh.raw_full[slot]);
+          bulk_g2s(raw + KT * (D / 2) + lane * rows * (D / 16), (i ? a.cache.v_scales : a.cache.k_scales) + row * (D / 16),
+                   rows * (D / 16), &sh.raw_full[slot]);
+        }
+      }
+      page = next;
+    }
+  }
+  // no copy may still be landing when the block ends
+  __syncwarp();
+  for (uint32_t j = n_raw > RAW ? n_raw - RAW : 0; j < n_raw; ++j) {
+    volatile int no_abort = 0;
+    mbar_wait(&sh.raw_full[j % RAW], (j / RAW) & 1, &no_abort, a.status);
+  }
+}
+
+// ---------------------------------------------------------------- products
+// One warp issues S = Q K^T and another O += P V, each with its own waits: an issue holds its warp
+// until the tensor core has taken the instruction, and one warp for both left the core idle for
+// the length of every wait. The whole warp takes the walk and the waits, so that descriptors are
+// the same in every lane (uniform registers); one elected lane issues.
+
+// row groups of a run (a form of one group has one)
+template <int D>
+MOE_DEV int run_groups(const KvAttnArgs& a, const Run& run) {
+  return !Tc<D>::pair && load_seq(a, run.b).n_q * a.G - run.tile * Tc<D>::rows > kHalf ? 2 : 1;
+}
+
+// TMEM and shared memory are given back only after every product is done with them
+MOE_DEV void drain(uint64_t* bar, int32_t* status) {
+  if (elect_one()) {
+    mma_commit(bar);
+    volatile int no_abort = 0;
+    mbar_wait(bar, 0, &no_abort, status);
+  }
+  __syncwarp();
+}
+
+template <int D>
+MOE_DEV void products_qk(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_t tmem, const uint8_t* s_q, const uint8_t* s_k) {
+  using C = Tc<D>;
+  constexpr int KT = C::kt, NS = C::stages;
+  constexpr uint32_t idesc = idesc_f16(kHalf, KT, false);
+  uint32_t tc = 0, n_s = 0, items[2] = {0, 0};  // key tiles, S, and runs of each group so far
+  bool ok = true;
+  Run run;
+  const uint64_t desc_q = sdesc_sw128(smem_u32(s_q)), desc_k = sdesc_sw128(smem_u32(s_k));
+  while (ok && walk.next(&run)) {
+    const int groups = run_groups<D>(a, run), n = run.u1 - run.u0;
+    for (int i = 0; i < n * groups; ++i, ++n_s) {
+      const int g = groups == 2 ? i & 1 : 0, j = groups == 2 ? i >> 1 : i;
+      const uint32_t t = tc + j, s = t % NS;
+      if (j == 0) ok = __all_sync(0xffffffffu, wait_soon(&sh.q_full[g], (g ? items[1] : items[0]) & 1, &sh.wait, a.status));
+      // once the scores before have been copied
+      ok = ok && wait_both(&sh.k_full[s], (t / NS) & 1, &sh.s_empty, (n_s & 1) ^ 1, &sh.wait, a.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dq = desc_q + ((g * (kHalf * D * 2)) >> 4), dk = desc_k + s * (C::tile_bytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t in = (kk % 4) * 32, bk = ((kk / 4) * (KT * 128) + in) >> 4;
+          if constexpr (C::pair)
+            mma_f16_ts(tmem + C::s_col, tmem + C::q_col + 8 * kk, dk + bk, idesc, kk ? 1u : 0u);
+          else
+            mma_f16_ss(tmem + C::s_col, dq + (((kk / 4) * (kHalf * 128) + in) >> 4), dk + bk, idesc, kk ? 1u : 0u);
+        }
+        mma_commit(&sh.s_full[g]);
+        if (g + 1 == groups) mma_commit(&sh.k_empty[s]);
+      }
+      __syncwarp();
+    }
+    tc += n;
+    items[0] += 1;
+    items[1] += groups - 1;
+  }
+  drain(&sh.drained[0], a.status);
+}
+
+template <int D>
+MOE_DEV void products_pv(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_t tmem, const uint8_t* s_v) {
+  using C = Tc<D>;
+  constexpr int KT = C::kt, NS = C::stages;
+  constexpr uint32_t idesc = idesc_f16(kHalf, D, true);
+  uint32_t tc = 0, used[2] = {0, 0};  // key tiles, and of each group, so far
+  bool ok = true;
+  Run run;
+  const uint64_t desc_v = sdesc_mn_sw128(smem_u32(s_v), KT * 128);
+  while (ok && walk.next(&run)) {
+    const int groups = run_groups<D>(a, run), n = run.u1 - run.u0;
+    for (int i = 0; i < n * groups; ++i) {
+      const int g = groups == 2 ? i & 1 : 0, j = groups == 2 ? i >> 1 : i;
+      const uint32_t t = tc + j, s = t % NS;
+      // the buffer of P and its turn
+      const uint32_t b = C::pair ? t & 1 : g, at = C::pair ? t >> 1 : (g ? used[1] : used[0]) + j;
+      ok = wait_both(&sh.p_full[b], at & 1, &sh.v_full[s], (t / NS) & 1, &sh.wait, a.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dv = desc_v + s * (C::tile_bytes >> 4);
+      const uint32_t p = tmem + C::p_col + b * (KT / 2), add = j ? 1u : 0u;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          mma_f16_ts(tmem + g * D, p + 8 * kk, dv + ((kk * 2048) >> 4), idesc, kk ? 1u : add);
+        mma_commit(&sh.pv_done[b]);
+        if (g + 1 == groups) mma_commit(&sh.v_empty[s]);
+      }
+      __syncwarp();
+    }
+    tc += n;
+    used[0] += n;
+    used[1] += (groups - 1) * n;
+  }
+  drain(&sh.drained[1], a.status);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Tc<D>::threads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
+  using C = Tc<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* s_k = smem;
-  uint8_t* s_v = s_k + NS * kTileBytes;
-  uint8_t* s_raw = s_v + NS * kTileBytes;
-  __shared__ uint64_t raw_full[RAW], raw_empty[RAW];
-  __shared__ uint32_t s_bad[RAW];  // groups of 16 keys whose page number is outside the cache
-  __shared__ uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  __shared__ uint64_t q_full, s_full, s_empty, p_full[2], pv_done[2], drained;
-  __shared__ uint32_t s_tmem;
-  __shared__ Patience s_wait;
-  __shared__ float s_x[2][kRows];
-  __shared__ int s_e[2][kRows];
-  __shared__ int s_idx;
+  uint8_t* s_q = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* s_k = s_q + C::q_bytes;
+  uint8_t* s_v = s_k + C::stages * C::tile_bytes;
+  uint8_t* s_raw = s_v + C::stages * C::tile_bytes;
+  __shared__ TcShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&k_full[s], EW);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], EW);
-      mbar_init(&v_empty[s], 1);
+    constexpr int EW = C::exp_warps / 2, soft = C::pair ? kSoftWarps : kSoftWarps / 2;
+    for (int s = 0; s < C::stages; ++s) {
+      mbar_init(&sh.k_full[s], EW);
+      mbar_init(&sh.k_empty[s], 1);
+      mbar_init(&sh.v_full[s], EW);
+      mbar_init(&sh.v_empty[s], 1);
     }
-    for (int i = 0; i < RAW; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], EW);
+    for (int i = 0; i < C::raw_slots; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], EW);
     }
-    mbar_init(&q_full, kSoftWarps);
-    mbar_init(&s_full, 1);
-    mbar_init(&s_empty, kSoftWarps);
+    mbar_init(&sh.s_empty, soft);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_full[i], kSoftWarps);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&sh.q_full[i], soft);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], soft);
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.drained[i], 1);
     }
-    mbar_init(&drained, 1);
     fence_barrier_init();
-    s_wait.abort = 0;
-    s_wait.limit = wait_limit_ns();
+    sh.wait.abort = 0;
+    sh.wait.limit = wait_limit_ns();
   }
-  if (warp == kMmaWarp) tmem_alloc(&s_tmem, 512);
+  if (warp == C::mma_warp) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = sh.tmem;
   MOE_PDL_PROLOGUE();
 
   // ---- this block's run of the work
@@ -342,7 +1016,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
   const long long total = walk.per_head * a.cache.Hkv;
   const int grid = (int)min((long long)gridDim.x, total);
   walk.at = walk.end = 0;
-  walk.start = start_cost(D);
+  walk.start = C::start_cost;
   if ((int)blockIdx.x < grid) {
     walk.at = total * blockIdx.x / grid;
     walk.end = total * (blockIdx.x + 1) / grid;
@@ -358,400 +1032,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnA
         lo += (n - 1) * step;
         hi = min(hi, lo + step);
       }
-      if (lane == 0) s_idx = lo;
+      if (lane == 0) sh.idx = lo;
     }
   }
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   __syncthreads();
-  walk.idx = s_idx;
+  walk.idx = sh.idx;
 
   if (warp < kSoftWarps) {
-    // ================================================================ softmax
-    more_registers<kSoftRegs>();
-    const int half = warp >> 2, quarter = warp & 3;  // half of the keys, of Q and of O
-    const int row = quarter * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    uint32_t tc = 0;  // key tiles so far
-    bool ok = true;
-    Run run;
-    while (ok && walk.next(&run)) {
-      const SeqSpan sq = load_seq(a, run.b);
-      const int rows = sq.n_q * a.G, rr = run.tile * kRows + row;
-      const bool live = rr < rows;
-      const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
-      const float ks = a.scale * (a.cache.k_ts ? a.cache.k_ts[run.h] : 1.0f) * kLog2e;
-      // ---- Q: this thread's half of the row
-      float fac;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride +
-                                                          (int64_t)head * D + half * (D / 2));
-        uint4 raw[D / 16];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-          mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
-          mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
-          mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
-          mx = __vmaxu2(mx, raw[i].w & 0x7FFF7FFFu);
-        }
-        s_e[half][row] = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;
-        named_bar_sync(5, kSoftWarps * 32);
-        const int e = max(max(s_e[0][row], s_e[1][row]), -100);
-        // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
-        const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
-        fac = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          uint32_t f[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t w[4] = {raw[4 * i + j].x, raw[4 * i + j].y, raw[4 * i + j].z, raw[4 * i + j].w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              f[4 * j + u] = pack_f16(bf16_to_f32(w[u] & 0xFFFFu) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
-          }
-          tmem_st16(tl + kQ + half * (D / 4) + 16 * i, f);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
-      }
-      const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
-      // keys that every row of the tile sees
-      const int first_tok = run.tile * kRows / a.G;
-      const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
-      float m = kNoMax;
-      uint64_t l2 = pack2(0.0f, 0.0f);
-      const uint64_t fac2 = pack2(fac, fac);
-      for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        // the scores, and the product that last read this tile's columns of P
-        if (tc >= 2)
-          ok = wait_both(&s_full, tc & 1, &pv_done[tc & 1], ((tc >> 1) - 1) & 1, &s_wait, a.status) && ok;
-        else
-          ok = __all_sync(0xffffffffu, wait_soon(&s_full, tc & 1, &s_wait, a.status)) && ok;
-        tc_fence_after();
-        uint32_t s[HK];
-#pragma unroll
-        for (int i = 0; i < HK; i += 32) tmem_ld32(tl + kS + half * HK + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty);
-        if (u * KT + KT > lim_min) {
-          const int left = lim - u * KT - half * HK;
-#pragma unroll
-          for (int i = 0; i < HK; ++i)
-            if (i >= left) s[i] = 0xff800000u;
-        }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < HK; i += 2)
-          mx4[(i / 2) & 3] = fmaxf(mx4[(i / 2) & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
-        // the two warps of these 32 rows decide together
-        if (bar_or(1 + quarter, 64, mx > m + kRaise || !ok)) {
-          s_x[half][row] = mx;
-          if (bar_or(1 + quarter, 64, !ok)) {
-            ok = false;
-            break;
-          }
-          const float top = fmaxf(fmaxf(s_x[0][row], s_x[1][row]), m);
-          if (u > run.u0) {
-            const float fix = ex2(m - top);
-            float a0, a1;
-            unpack2(l2, a0, a1);
-            l2 = pack2(a0 * fix, a1 * fix);
-            ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
-            tc_fence_after();
-            if (ok) {
-#pragma unroll 1
-              for (int c = 0; c < D / 2; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tl + kO + half * (D / 2) + c, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-                tmem_st32(tl + kO + half * (D / 2) + c, o);
-              }
-              tmem_st_wait();
-            }
-          }
-          m = top;
-          bar_or(1 + quarter, 64, false);  // s_x is free again
-        }
-        const uint64_t nm2 = pack2(-m, -m);
-        const uint32_t tp = tl + kP + (tc & 1) * (KT / 2) + half * (HK / 2);
-#pragma unroll
-        for (int q = 0; q < HK / 32; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
-            float x0, x1;
-            if (D < 256 && i % 4 == 3) {  // a quarter of them past the special-function unit, the busiest one here
-              ex2_pair(x, x0, x1);
-            } else {
-              unpack2(x, x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-            }
-            l2 = add2(l2, pack2(x0, x1));
-            p[i] = pack_f16(x0, x1);
-          }
-          tmem_st16(tp + 16 * q, p);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tc & 1]);
-      }
-      // ---- the run's result
-      float l0, l1;
-      unpack2(l2, l0, l1);
-      s_x[half][row] = l0 + l1;
-      if (ok) ok = __all_sync(0xffffffffu, wait_soon(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &s_wait, a.status));
-      tc_fence_after();
-      if (bar_or(5, kSoftWarps * 32, !ok)) break;
-      const float ll = s_x[0][row] + s_x[1][row];
-      const bool whole = run.u0 == 0 && run.u1 == run.n_units;
-      const float vts = a.cache.v_ts ? a.cache.v_ts[run.h] : 1.0f;
-      const float f = !whole ? 1.0f : ll > 0.0f ? vts / ll : (ll == 0.0f ? 0.0f : ll);
-      const int64_t out_row = (int64_t)(sq.q0 + tok) * a.Hq + head;
-      const int side = run.u0 > 0 ? 0 : 1;
-      float* part = a.partial + ((size_t)blockIdx.x * 2 + side) * a.part_stride;
-#pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tl + kO + half * (D / 2) + c, o);
-        tmem_ld_wait();
-        if (whole) {
-          if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + half * (D / 2) + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * j]) * f,
-                                                               __uint_as_float(o[8 * i + 2 * j + 1]) * f);
-                w[j] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(part + 2 * kRows + row * D + half * (D / 2) + c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                 __uint_as_float(o[4 * i + 3]));
-        }
-      }
-      if (half == 0) {
-        if (!whole) {
-          part[row] = m;
-          part[kRows + row] = ll;
-        } else if (live && a.lse) {
-          a.lse[out_row] = ll == 0.0f ? -INFINITY : (m + log2f(ll)) * kLn2;
-        }
-      }
-      if (!whole && side == 1 && threadIdx.x == 0) {
-        int last = blockIdx.x + 1;
-        while (total * (last + 1) / grid < run.end) ++last;
-        a.meta[blockIdx.x] = make_int4(run.b, run.h, run.tile * kRows, last);
-      }
-      tc_fence_before();
-      named_bar_sync(5, kSoftWarps * 32);  // s_x and s_e are free again, O has been read
-    }
-  } else if (warp < kMmaWarp) {
-    // ================================================================ expanders
-    // 16 elements (8 bytes of codes, one scale) a lane and step, lanes side by side in the raw
-    // slot. A step is a whole number of 8 rows on, so a lane keeps its place in the swizzle; of its
-    // two 16-byte stores, lanes that would meet in a bank take the second one first.
-    fewer_registers<kExpRegs>();
-    constexpr int P = D / 16;                 // lanes of a row
-    constexpr int STEPS = KT * P / (32 * EW), ROWS = 32 / P * EW;  // rows of a step
-    static_assert(ROWS % 8 == 0, "a lane keeps its row modulo 8");
-    const int pw = (warp - kSoftWarps) % EW;
-    const bool is_v = warp >= kSoftWarps + EW;
-    uint64_t* full = is_v ? v_full : k_full;
-    uint64_t* empty = is_v ? v_empty : k_empty;
-    const int row0 = (pw * 32 + lane) / P, part = lane % P;
-    const bool swap = D >= 128 && (part & 4);
-    const uint32_t off0 = (part >> 2) * (KT * 128) + row0 * 128 + (((((part & 3) << 1) | (swap ? 1 : 0)) ^ (row0 & 7)) << 4);
-    const uint32_t off1 = off0 ^ 16;
-    uint32_t tc = 0;
-    bool ok = true;
-    Run run;
-    while (ok && walk.next(&run)) {
-      const int ctx = load_seq(a, run.b).ctx;
-#pragma unroll 1
-      for (int u = run.u0; u < run.u1; ++u, ++tc) {
-        const uint32_t n_raw = 2 * tc + (is_v ? 1 : 0), slot = n_raw % RAW, s = tc % NS;
-        ok = wait_both(&raw_full[slot], (n_raw / RAW) & 1, &empty[s], ((tc / NS) & 1) ^ 1, &s_wait, a.status);
-        if (!ok) break;
-        const uint8_t* raw = s_raw + slot * raw_bytes(D);
-        const uint32_t bad = s_bad[slot];
-        const int left = ctx - u * KT;
-        uint2 codes[STEPS];
-        uint32_t scales[STEPS];
-#pragma unroll
-        for (int step = 0; step < STEPS; ++step) {
-          codes[step] = reinterpret_cast<const uint2*>(raw)[(step * EW + pw) * 32 + lane];
-          scales[step] = (raw + KT * (D / 2))[(step * EW + pw) * 32 + lane];
-        }
-        if (bad || left < KT) {  // keys past the end, and pages outside the cache, count as zeros
-#pragma unroll
-          for (int step = 0; step < STEPS; ++step) {
-            const int row = row0 + step * ROWS;
-            if (row >= left || ((bad >> (row / 16)) & 1u)) scales[step] = 0u;
-          }
-        }
-        uint8_t* dst = (is_v ? s_v : s_k) + s * kTileBytes;
-#pragma unroll
-        for (int step = 0; step < STEPS; ++step) {
-          const uint32_t w0 = swap ? codes[step].y : codes[step].x, w1 = swap ? codes[step].x : codes[step].y;
-          const uint32_t sc = e4m3x2_to_f16x2(scales[step] * 0x0101u);
-          uint32_t f[4];
-          e2m1x8_to_f16x2x4(w0, f);
-          *reinterpret_cast<uint4*>(dst + off0 + step * (ROWS * 128)) =
-              make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
-          e2m1x8_to_f16x2x4(w1, f);
-          *reinterpret_cast<uint4*>(dst + off1 + step * (ROWS * 128)) =
-              make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&raw_empty[slot]);
-          mbar_arrive(&full[s]);
-        }
-      }
-    }
+    more_registers<C::soft_regs>();
+    if constexpr (C::pair)
+      softmax_pair<D>(a, sh, walk, tmem, total, grid);
+    else
+      softmax_rows<D>(a, sh, walk, tmem, s_q, total, grid);
+  } else if (warp < C::mma_warp) {
+    fewer_registers<C::exp_regs>();
+    expand<D>(a, sh, walk, s_k, s_v, s_raw);
   } else {
-    fewer_registers<kLastRegs>();
-    if (warp == kLoadWarp) {
-      // ================================================================ loader
-      // a lane copies one page's part of the tile: at most KT / 16 pages
-      uint32_t n_raw = 0;
-      bool ok = true;
-      Run run;
-      const int ps = a.cache.page_size;
-      const int rows = min(ps, KT);               // of a copy
-      const int copies = KT / rows;               // of a slot
-      while (ok && walk.next(&run)) {
-        const int ctx = load_seq(a, run.b).ctx;
-        const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
-        auto page_of = [&](int u) {
-          const int t = u * KT + lane * rows;
-          return lane < copies && t < ctx ? __ldg(table + (t >> a.page_shift)) : 0;
-        };
-        int page = page_of(run.u0);
-        for (int u = run.u0; u < run.u1 && ok; ++u) {
-          const int next = page_of(u + 1);
-          const int t = u * KT + lane * rows;
-          const bool wanted = lane < copies && t < ctx;
-          const bool good = wanted && page >= 0 && page < a.cache.n_pages;
-          if (wanted && !good) atomicExch(a.status, kStatusInvalid);
-          const uint32_t bads = __ballot_sync(0xffffffffu, wanted && !good), goods = __ballot_sync(0xffffffffu, good);
-          const int64_t row = ((int64_t)page * a.cache.Hkv + run.h) * ps + (t & (ps - 1));
-          uint32_t bad = 0;  // a copy of `rows` keys is rows / 16 groups of 16
-          for (int j = 0; bads && j < copies; ++j)
-            if ((bads >> j) & 1u) bad |= ((1u << (rows / 16)) - 1u) << (j * (rows / 16));
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i, ++n_raw) {  // K, then V
-            const uint32_t slot = n_raw % RAW;
-            ok = __all_sync(0xffffffffu, wait_soon(&raw_empty[slot], ((n_raw / RAW) & 1) ^ 1, &s_wait, a.status));
-            if (!ok) break;
-            uint8_t* raw = s_raw + slot * raw_bytes(D);
-            if (lane == 0) {
-              s_bad[slot] = bad;
-              mbar_arrive_expect_tx(&raw_full[slot], __popc(goods) * rows * (D / 2 + D / 16));
-            }
-            __syncwarp();
-            if (good) {
-              bulk_g2s(raw + lane * rows * (D / 2), (i ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2), rows * (D / 2),
-                       &raw_full[slot]);
-              bulk_g2s(raw + KT * (D / 2) + lane * rows * (D / 16), (i ? a.cache.v_scales : a.cache.k_scales) + row * (D / 16),
-                       rows * (D / 16), &raw_full[slot]);
-            }
-          }
-          page = next;
-        }
-      }
-      // no copy may still be landing when the block ends
-      __syncwarp();
-      for (uint32_t j = n_raw > RAW ? n_raw - RAW : 0; j < n_raw; ++j) {
-        volatile int no_abort = 0;
-        mbar_wait(&raw_full[j % RAW], (j / RAW) & 1, &no_abort, a.status);
-      }
-    } else if (warp == kMmaWarp) {
-      // ================================================================ MMA
-      // The whole warp takes the walk and the waits, so that descriptors are the same in every
-      // lane (uniform registers); one elected lane issues.
-      constexpr uint32_t idesc_qk = idesc_f16(kRows, KT, false), idesc_pv = idesc_f16(kRows, D, true);
-      uint32_t tc = 0, items = 0;
-      bool ok = true;
-      Run run;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, wait_soon(bar, parity, &s_wait, a.status));
-      };
-      const uint64_t desc_k = sdesc_sw128(smem_u32(s_k)), desc_v = sdesc_mn_sw128(smem_u32(s_v), KT * 128);
-      while (ok && walk.next(&run)) {
-        wait(&q_full, items & 1);
-        ++items;
-        const int n = run.u1 - run.u0;
-        for (int j = 0; j <= n && ok; ++j) {
-          if (j < n) {  // S = Q K^T of tile j, once the scores of the tile before have been read
-            const uint32_t t = tc + j, s = t % NS;
-            ok = ok && wait_both(&k_full[s], (t / NS) & 1, &s_empty, (t & 1) ^ 1, &s_wait, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t desc = desc_k + s * (kTileBytes >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk / 4) * (KT * 128) + (kk % 4) * 32) >> 4;
-                mma_f16_ts(tmem + kS, tmem + kQ + 8 * kk, desc + off, idesc_qk, kk ? 1u : 0u);
-              }
-              mma_commit(&s_full);
-              mma_commit(&k_empty[s]);
-            }
-            __syncwarp();
-          }
-          if (j > 0) {  // O += P V of tile j - 1
-            const uint32_t t = tc + j - 1, s = t % NS;
-            ok = wait_both(&p_full[t & 1], (t >> 1) & 1, &v_full[s], (t / NS) & 1, &s_wait, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t desc = desc_v + s * (kTileBytes >> 4);
-            const uint32_t p = tmem + kP + (t & 1) * (KT / 2), add = j > 1 ? 1u : 0u;
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < KT / 16; ++kk)
-                mma_f16_ts(tmem + kO, p + 8 * kk, desc + ((kk * 2048) >> 4), idesc_pv, kk ? 1u : add);
-              mma_commit(&pv_done[t & 1]);
-              mma_commit(&v_empty[s]);
-            }
-            __syncwarp();
-          }
-        }
-        tc += n;
-      }
-      // TMEM and shared memory are given back only after every product is done with them
-      if (elect_one()) {
-        mma_commit(&drained);
-        volatile int no_abort = 0;
-        mbar_wait(&drained, 0, &no_abort, a.status);
-      }
-      __syncwarp();
+    fewer_registers<C::last_regs>();
+    if (warp == C::load_warp) {
+      load_raw<D>(a, sh, walk, s_raw);
+    } else if (warp == C::mma_warp) {
+      products_qk<D>(a, sh, walk, tmem, s_q, s_k);
+    } else if (warp == C::mma_warp + 1) {
+      products_pv<D>(a, sh, walk, tmem, s_v);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == C::mma_warp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -777,10 +1086,10 @@ __global__ void __launch_bounds__(256) kv_attn_tc_join_kernel(const KvAttnArgs a
     const float pm = p[row], top = fmaxf(mm, pm);
     const float f0 = ex2(mm - top), f1 = ex2(pm - top);
     mm = top;
-    ll = ll * f0 + p[kRows + row] * f1;
+    ll = ll * f0 + p[Tc<D>::rows + row] * f1;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float2 v = reinterpret_cast<const float2*>(p + 2 * kRows + row * D)[j * 32 + lane];
+      const float2 v = reinterpret_cast<const float2*>(p + 2 * Tc<D>::rows + row * D)[j * 32 + lane];
       acc[j].x = acc[j].x * f0 + v.x * f1;
       acc[j].y = acc[j].y * f0 + v.y * f1;
     }
@@ -797,17 +1106,18 @@ __global__ void __launch_bounds__(256) kv_attn_tc_join_kernel(const KvAttnArgs a
 
 template <int D>
 cudaError_t launch_tc(const KvAttnArgs& a, int num_sms, cudaStream_t st) {
-  cudaError_t e = launch_pdl(kv_attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, key_tile(D), start_cost(D));
+  using C = Tc<D>;
+  cudaError_t e = launch_pdl(kv_attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, C::rows, C::kt, C::start_cost);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kv_attn_tc_kernel<D>, dim3(num_sms), dim3(kTcThreads), tc_smem(D), st, a);
+  e = launch_pdl(kv_attn_tc_kernel<D>, dim3(num_sms), dim3(C::threads), C::smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_attn_tc_join_kernel<D>, dim3(num_sms, kRows / 8), dim3(256), 0, st, a);
+  return launch_pdl(kv_attn_tc_join_kernel<D>, dim3(num_sms, C::rows / 8), dim3(256), 0, st, a);
 }
 
 }  // namespace
 
-size_t kv_attn_tc_part_floats(int D) { return (size_t)kRows * (D + 2); }
-int kv_attn_tc_max_tiles(int64_t T, int n_seqs, int G) { return (int)(T * G / kRows + n_seqs + 1); }
+size_t kv_attn_tc_part_floats(int D) { return (size_t)(D == 256 ? Tc<256>::rows : Tc<128>::rows) * (D + 2); }
+int kv_attn_tc_max_tiles(int64_t T, int n_seqs, int G) { return (int)(T * G / kHalf + n_seqs + 1); }
 size_t kv_attn_tc_tiles_bytes(int64_t T, int n_seqs, int G) {
   return (size_t)kv_attn_tc_max_tiles(T, n_seqs, G) * sizeof(RowTile);
 }
@@ -819,8 +1129,8 @@ static cudaError_t attributes_tc() {
   cudaFuncAttributes at;
   cudaError_t e = cudaFuncGetAttributes(&at, kv_attn_tc_kernel<D>);
   if (e != cudaSuccess) return e;
-  if (at.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;  // the roles' shares would not add up
-  return cudaFuncSetAttribute(kv_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem(D));
+  if (at.numRegs != Tc<D>::launch_regs) return cudaErrorInvalidKernelImage;  // the roles' shares would not add up
+  return cudaFuncSetAttribute(kv_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::smem);
 }
 
 cudaError_t init_kv_attn_tc_attributes() {

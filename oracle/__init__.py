@@ -31,6 +31,9 @@ oracle takes the plainest reading, listed in each function's docstring:
      expert's token rows are quantised with its own static tensor scale in_gu[e] and its h
      with in_dn[e], instead of the per-call dynamic scale and 1.0.
 
+kv.py holds the readings of attention over an NVFP4 key/value cache (K1 to K4), which the pages
+name only as a cache; all of it in float64.
+
 Precision: float32 where the reading fixes float32 (quantiser steps, logits, routing
 weights, h), float64 elsewhere (dot products, combine).
 
