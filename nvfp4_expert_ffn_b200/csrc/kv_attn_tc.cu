@@ -264,29 +264,6 @@ MOE_DEV float max3(float a, float b, float c) {
   return d;
 }
 
-// 2^x for a pair, without the special-function unit: x = n + f with n whole and |f| <= 1/2, a
-// polynomial for 2^f (degree 5, least maximum relative error 7.5e-8 by Lawson's iteration), n
-// added to its exponent. x is taken as at least -126 (2^-126 rounds to 0 in float16).
-MOE_DEV void ex2_pair(uint64_t x, float& y0, float& y1) {
-  float x0, x1;
-  unpack2(x, x0, x1);
-  x = pack2(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
-  const uint64_t magic = pack2(12582912.0f, 12582912.0f);  // 1.5 * 2^23: the sum's last bit is 1
-  const uint64_t t = add2(x, magic);
-  const uint64_t f = add2(x, mul2(add2(t, pack2(-12582912.0f, -12582912.0f)), pack2(-1.0f, -1.0f)));
-  uint64_t p = pack2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
-  p = fma2(p, f, pack2(9.675541892647743e-3f, 9.675541892647743e-3f));
-  p = fma2(p, f, pack2(5.550713092088699e-2f, 5.550713092088699e-2f));
-  p = fma2(p, f, pack2(2.4022120237350464e-1f, 2.4022120237350464e-1f));
-  p = fma2(p, f, pack2(6.931469440460205e-1f, 6.931469440460205e-1f));
-  p = fma2(p, f, pack2(1.0000001192092896f, 1.0000001192092896f));
-  float p0, p1, t0, t1;
-  unpack2(p, p0, p1);
-  unpack2(t, t0, t1);
-  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
-
 // Waits for two barriers at once, every other lane for the second (a wait that is over at once
 // still costs the round trip). For a whole warp; the same answer in all lanes.
 MOE_DEV bool wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1, Patience* w, int32_t* status) {
@@ -460,13 +437,9 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
         for (int i = 0; i < 16; ++i) {
           const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
           float x0, x1;
-          if (D < 256 && i % 4 == 3) {  // a quarter of them past the special-function unit, the busiest one here
-            ex2_pair(x, x0, x1);
-          } else {
-            unpack2(x, x0, x1);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-          }
+          unpack2(x, x0, x1);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
           l2 = add2(l2, pack2(x0, x1));
           p[i] = pack_f16(x0, x1);
         }
@@ -656,13 +629,9 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
         for (int i = 0; i < 16; ++i) {
           const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
           float x0, x1;
-          if (i % 4 == 3) {  // a quarter of them past the special-function unit, the busiest one here
-            ex2_pair(x, x0, x1);
-          } else {
-            unpack2(x, x0, x1);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-          }
+          unpack2(x, x0, x1);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
           l2 = add2(l2, pack2(x0, x1));
           p[i] = pack_f16(x0, x1);
         }
