@@ -385,3 +385,145 @@ def test_steps_through_the_cache_match_one_prompt():
         ref, e, wt, s = okv.attention(qr[i:i + 1], kk[:i + 1], vv[:i + 1], D ** -0.5, False)
         tol, _ = _attn_bounds(ref, wt, s, e, i + 1, np.abs(vv).max(), D)
         assert np.all(np.abs(got[i] - ref[0]) <= tol[0]), i
+
+
+# ---------------------------------------------------------------- edges of the kernels' own units
+
+@pytest.mark.parametrize("D,Hkv,G", [(64, 1, 1), (64, 1, 14), (128, 2, 4), (128, 1, 5), (256, 2, 8), (256, 1, 3)])
+@pytest.mark.parametrize("past", [0, 1, 126, 127, 128, 300])
+def test_attention_around_tiles_of_rows_and_keys(D, Hkv, G, past):
+    """Rows a key head just below, at and above 32 (where the other kernel takes over), 128 and 256
+    (row tiles), contexts around multiples of 64 and 128, in one call."""
+    q_lens = sorted({max(1, r // G + e) for r in (32, 128, 256) for e in (0, 1)})
+    c = Case(D, Hkv, G, 16, q_lens, [n + past for n in q_lens], D + G + past, extra_rows=1)
+    c.check(rows=5)
+
+
+def test_attention_few_rows_over_a_long_cache_are_split():
+    """One row tile whose keys go to many blocks, with 100, 160 and 300 rows."""
+    for D, G, n in ((128, 4, 25), (128, 4, 40), (64, 3, 100), (256, 4, 40)):
+        Case(D, 1, G, 64, [n], [20011], D + n).check(rows=4)
+
+
+def test_attention_more_sequences_than_the_plan_takes_at_once():
+    rng = np.random.default_rng(7)
+    n = 1100  # the plan scans 1024 at a time
+    q_lens = [int(x) for x in rng.integers(0, 3, n)]
+    for b in (0, 500, 1023, 1024, 1099):
+        q_lens[b] = 40
+    Case(64, 1, 2, 16, q_lens, [x + int(rng.integers(0, 30)) for x in q_lens], 8).check(rows=4)
+
+
+def test_attention_sequences_longer_than_max_q():
+    """max_q only picks the kernels: a bound that is too low costs time, not results."""
+    c = Case(128, 2, 4, 32, [3, 70], [50, 70], 9)
+    want, _ = c.run()
+    got, _ = c.run(max_q=1)
+    assert B.moe_get_device_status() == 0
+    tol = 2 * (2.0 ** -8 + 2.0 ** -9)  # both are roundings of nearly the same value: see check()
+    c.check()
+    assert np.all(np.abs(_np(got) - _np(want)) <= tol * np.maximum(np.abs(_np(want)), np.abs(_np(got)).max()))
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 3.0])
+@pytest.mark.parametrize("n", [1, 50])
+def test_attention_scales(n, scale):
+    """A negative scale turns the order of the keys round, a scale of zero weighs them equally."""
+    c = Case(64, 1, 2, 16, [n], [130], 10)
+    out, lse = torch.empty(n, 2, 64, dtype=torch.bfloat16, device=DEV), torch.empty(n, 2, device=DEV)
+    B.nvfp4_kv_attention(_gpu(c.q).bfloat16(), *c.args, n, c.gcache, scale, False, out, lse, c.ws)
+    k, v = c.cache.read("k", c.slots[0]), c.cache.read("v", c.slots[0])
+    ref, e, w, s = okv.attention(c.q, k, v, scale, False)
+    tol, tol_e = _attn_bounds(ref, w, np.abs(s), e, 130, np.abs(v).max(), 64)
+    assert np.all(np.abs(_np(out) - ref) <= tol) and np.all(np.abs(lse.cpu().numpy() - e) <= tol_e)
+
+
+def test_attention_without_tensor_scales_and_with_negative_ones():
+    for kts, vts in ((None, None), (-0.002, -0.5)):
+        for n in (1, 50):
+            c = Case(128, 1, 2, 16, [n], [90], 11)
+            for name, ts in (("k", kts), ("v", vts)):
+                c.cache.ts[name][:] = 1.0 if ts is None else ts
+            g = c.gcache
+            one = lambda x: None if x is None else torch.full((1,), x, device=DEV)  # noqa: E731
+            c.gcache = B.KVCache(g.k_codes, g.k_scales, g.v_codes, g.v_scales, one(kts), one(vts))
+            c.q = okv.to_bf16(c.q * (0.002 if kts is None else 1.0))
+            c.check()
+
+
+def test_attention_two_streams_at_once():
+    """Two calls with a workspace each on two streams, and a small call with the workspace of a
+    large one between two large ones: the same bits as alone."""
+    a, b = Case(128, 2, 4, 32, [300, 1, 40], [700, 300, 40], 12), Case(128, 2, 4, 32, [1] * 9, list(range(1, 900, 100)), 13)
+    want = [x.run()[0] for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for x, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append(x.run()[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    own, b.ws = b.ws, a.ws
+    assert own.numel() <= a.ws.numel()
+    for x, w in ((a, want[0]), (b, want[1]), (a, want[0])):
+        assert torch.equal(x.run()[0], w)
+    assert B.moe_get_device_status() == 0
+
+
+def test_calls_without_tokens_or_sequences():
+    cache = B.KVCache.allocate(1, 16, 1, 64)
+    e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    i = torch.empty(0, dtype=torch.int32, device=DEV)
+    B.moe_qk_norm_rope(e, None, i, B.QKPrep(), e.clone(), None)
+    B.nvfp4_kv_append(None, e[:, :1], e[:, :1], i, i, B.QKPrep(), cache, None)
+    B.nvfp4_kv_read(cache, i, torch.empty(0, 1, 64, device=DEV), None)
+    q = torch.ones(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, 3.0)
+    ws = torch.empty(B.nvfp4_kv_attention_workspace(3, 1, 3, 2, cache), dtype=torch.uint8, device=DEV)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    B.nvfp4_kv_attention(q, zero, zero[:1], zero[:1, None], 1, cache, 1.0, True, out, None, ws)
+    assert torch.all(out == 3.0) and B.moe_get_device_status() == 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** -100, 2.0 ** 60])
+def test_norm_of_huge_and_tiny_rows(size):
+    """The sum of squares leaves float32's range; the normalised row does not."""
+    rng = np.random.default_rng(14)
+    x = okv.to_bf16(_bf16(rng, 6, 3, 128, spread=0) * size)
+    pos = np.arange(6, dtype=np.int32) * 1000
+    f = (1e4 ** (-np.arange(64) / 64)).astype(np.float32)
+    w = rng.uniform(0.5, 1.5, 128).astype(np.float32)
+    out, ko = (torch.empty(6, 3, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    B.moe_qk_norm_rope(_gpu(x).bfloat16(), _gpu(x).bfloat16(), _gpu(pos), B.QKPrep(_gpu(w), _gpu(w), 0.0, _gpu(f)), out, ko)
+    ref = okv.norm_rope(x, pos, w, 0.0, f)
+    top = np.sqrt(2) * np.abs(okv.norm_rope(np.abs(x), pos, w, 0.0)).max(axis=-1, keepdims=True)
+    for got, err in ((out, 2.0 ** -24 * (128 / 16 + 16) * top), (ko, 0.0)):  # the terms of test_norm_rope
+        assert np.all(np.abs(_np(got) - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -23) + err + 1e-37)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,T", [(64, 14, 2, 4099), (128, 5, 3, 2053), (256, 3, 1, 1027)])
+def test_many_tokens_match_few(D, Hq, Hkv, T):
+    """Odd numbers of tokens through the writer of many tokens, and the same in slices of seven
+    through the writer of few: the same cache bit for bit (keys and values; queries are compared
+    with the oracle in test_norm_rope)."""
+    c = _append_case(D, Hkv, 16, T, 15, Hq=Hq)
+    ts = _gpu(c["kts"]), _gpu(c["vts"])
+    prep = B.QKPrep(_gpu(c["w"]), _gpu(c["w"]), 1e-6, _gpu(c["f"]), True, 0.7)
+    k, v, q = (_gpu(c[n]).bfloat16() for n in "kvq")
+    pos, slots = _gpu(c["pos"]), _gpu(c["slots"])
+    caches = [B.KVCache.allocate(c["n_pages"], 16, Hkv, D, *ts) for _ in range(2)]
+    for x in caches:
+        for t in (x.k_codes, x.k_scales, x.v_codes, x.v_scales):
+            t.fill_(0x11)
+    qo, qs = torch.empty_like(q), torch.empty_like(q)
+    B.nvfp4_kv_append(q, k, v, pos, slots, prep, caches[0], qo)
+    for i in range(0, T, 7):
+        s = slice(i, min(i + 7, T))
+        B.nvfp4_kv_append(q[s], k[s], v[s], pos[s], slots[s], prep, caches[1], qs[s])
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
+    # two roundings to bf16 of values that differ by float32 roundings: at most a bf16 step
+    assert np.all(np.abs(_np(qo) - _np(qs)) <= 2.0 ** -7 * np.maximum(np.abs(_np(qo)), np.abs(_np(qs))) + 2.0 ** -18)
+    assert B.moe_get_device_status() == 0
