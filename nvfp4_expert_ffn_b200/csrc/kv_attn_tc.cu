@@ -309,6 +309,27 @@ struct Walk {
 };
 
 
+// The run after this one and the start of its queries' way here, before the wait for the last
+// product: four dependent loads (tile, sequence, query rows) otherwise stand between two runs.
+template <int D>
+struct NextRun {
+  Run run;
+  SeqSpan sq;
+  bool more;
+
+  MOE_DEV void get(const KvAttnArgs& a, Walk& walk, int row, int half) {
+    more = walk.next(&run);
+    if (!more) return;
+    sq = load_seq(a, run.b);
+    const int rr = run.tile * Tc<D>::rows + row;
+    if (rr >= sq.n_q * a.G) return;
+    const int tok = rr / a.G;
+    const uint16_t* src = a.q + (int64_t)(sq.q0 + tok) * a.q_stride + (int64_t)(run.h * a.G + rr - tok * a.G) * D;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src + half * 128));
+    if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+  }
+};
+
 // ---------------------------------------------------------------- softmax, two threads a row
 template <int D>
 MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_t tmem, long long total, int grid) {
@@ -320,9 +341,11 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
   const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
   uint32_t tc = 0;  // key tiles so far
   bool ok = true;
-  Run run;
-  while (ok && walk.next(&run)) {
-    const SeqSpan sq = load_seq(a, run.b);
+  NextRun<D> next;
+  next.get(a, walk, row, half);
+  while (ok && next.more) {
+    const Run run = next.run;
+    const SeqSpan sq = next.sq;
     const int rows = sq.n_q * a.G, rr = run.tile * kHalf + row;
     const bool live = rr < rows;
     const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
@@ -451,6 +474,7 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       if (lane == 0) mbar_arrive(&sh.p_full[tc & 1]);
     }
     // ---- the run's result
+    next.get(a, walk, row, half);
     float l0, l1;
     unpack2(l2, l0, l1);
     sh.x[half][row] = l0 + l1;
@@ -526,11 +550,16 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
   const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16), to = tl + g * D, tp = tl + C::p_col + g * (KT / 2);
   uint32_t tc = 0;  // key tiles of this group so far
   bool ok = true;
-  Run run;
-  while (ok && walk.next(&run)) {
-    const SeqSpan sq = load_seq(a, run.b);
+  NextRun<D> next;
+  next.get(a, walk, g * kHalf + row, 0);
+  while (ok && next.more) {
+    const Run run = next.run;
+    const SeqSpan sq = next.sq;
     const int rows = sq.n_q * a.G, n = run.u1 - run.u0, first_row = run.tile * C::rows + g * kHalf;
-    if (g == 1 && rows - run.tile * C::rows <= kHalf) continue;
+    if (g == 1 && rows - run.tile * C::rows <= kHalf) {
+      next.get(a, walk, g * kHalf + row, 0);
+      continue;
+    }
     const int rr = first_row + row;
     const bool live = rr < rows;
     const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
@@ -647,7 +676,9 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       if (!ok) break;
       if (lane == 0) mbar_arrive(&sh.p_full[g]);
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
+    if (!ok) break;
+    next.get(a, walk, g * kHalf + row, 0);
+    ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
     if (!ok) break;
     tc_fence_after();
     // ---- the run's result
