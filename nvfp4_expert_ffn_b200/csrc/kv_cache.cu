@@ -307,11 +307,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
   });
 
   // ---- queries, in float32, two elements an instruction
-  if (a.Hq) each_row<4>(a.q + tok * a.q_stride, a.Hq, first(nk + nv), sub, step, D, e0, [&](const uint4& p, int h, bool live) {
+  if (a.Hq) each_row<2>(a.q + tok * a.q_stride, a.Hq, first(nk + nv), sub, step, D, e0, [&](const uint4& p, int h, bool live) {
     uint64_t y[4];
     unpack8x2(p, y);
     float rs = 1.0f;
-    double far_rs = 0.0;
+    float up = 1.0f;
     if (a.q_weight) {
       uint64_t s2 = mul2(y[0], y[0]);
 #pragma unroll
@@ -322,33 +322,29 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       rs = rsqrtf(ss * (1.0f / D) + (float)a.eps);
-      const bool far = !(ss < 1e36f && ss > 1e-30f) && live;  // squares near the ends of float32's range
-      if (__any_sync(0xffffffffu, far)) {
-        double sd = 0.0;
-        float v[8];
-        unpack8(p, v);
+      const bool far = !(ss < 1e36f && (ss > 1e-30f || a.eps > 1e-25)) && live;  // squares near the ends of float32's range
+      if (__any_sync(0xffffffffu, far)) {  // once more, 2^100 larger or smaller
+        if (far) up = ss > 1.0f ? 0x1p-100f : 0x1p100f;
+        const uint64_t u2 = pack2(up, up);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sd = fma((double)v[i], (double)v[i], sd);
+        for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], u2);
+        s2 = mul2(y[0], y[0]);
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-        if (far) {
-          far_rs = norm_factor(sd, D, a.eps);
-          rs = 1.0f;
-        }
+        for (int i = 1; i < 4; ++i) s2 = fma2(y[i], y[i], s2);
+        unpack2(s2, sa, sb);
+        ss = sa + sb;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        rs = rsqrtf(ss * (1.0f / D) + (float)a.eps * up * up);
       }
     }
     const uint4 pp = hop ? partner(p) : beside(p);
     uint64_t q[4];
     unpack8x2(pp, q);
-    if (far_rs != 0.0) {
+    if (up != 1.0f) {
+      const uint64_t u2 = pack2(up, up);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float u, v;
-        unpack2(y[i], u, v);
-        y[i] = pack2((float)(u * far_rs), (float)(v * far_rs));
-        unpack2(q[i], u, v);
-        q[i] = pack2((float)(u * far_rs), (float)(v * far_rs));
-      }
+      for (int i = 0; i < 4; ++i) q[i] = mul2(q[i], u2);
     }
     const uint64_t* ta = reinterpret_cast<const uint64_t*>(s_qa[t]) + lane;
     const uint64_t* tb = reinterpret_cast<const uint64_t*>(s_qb[t]) + lane;
