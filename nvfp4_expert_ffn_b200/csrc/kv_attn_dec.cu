@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
       const bool good = page >= 0 && page < a.cache.n_pages;
       const uint32_t bads = __ballot_sync(0xffffffffu, page != -2 && !good), goods = __ballot_sync(0xffffffffu, good);
       if (lane == 0) {
-        if (bads) atomicExch(a.status, kStatusInvalid);
+        if (bads) atomicMax(a.status, kStatusInvalid);
         s_bad[warp][slot] = copies == 1 ? (bads ? 3u : 0u) : bads & 3u;
         mbar_arrive_expect_tx(&s_full[warp][slot], (__popc(goods & 0x0Fu) * (D / 2) + __popc(goods & 0xF0u) * (D / 16)) * rows_copy);
       }

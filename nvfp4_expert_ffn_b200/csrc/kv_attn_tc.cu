@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttn
   }
   __syncthreads();  // (and with it the writes above, for this block)
   // more tiles than T rows can have: cu_q is not ascending
-  if (at > a.max_tiles && threadIdx.x == 0) atomicExch(a.status, kStatusInvalid);
+  if (at > a.max_tiles && threadIdx.x == 0) atomicMax(a.status, kStatusInvalid);
   const int n_tiles = (int)min(at, (long long)a.max_tiles);
   // 2. their work
   at = 0;
@@ -832,7 +832,7 @@ MOE_DEV void load_raw(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_
       const int t = u * KT + lane * rows;
       const bool wanted = lane < copies && t < ctx;
       const bool good = wanted && page >= 0 && page < a.cache.n_pages;
-      if (wanted && !good) atomicExch(a.status, kStatusInvalid);
+      if (wanted && !good) atomicMax(a.status, kStatusInvalid);
       const uint32_t bads = __ballot_sync(0xffffffffu, wanted && !good), goods = __ballot_sync(0xffffffffu, good);
       const int64_t row = ((int64_t)page * a.cache.Hkv + run.h) * ps + (t & (ps - 1));
       uint32_t bad = 0;  // a copy of `rows` keys is rows / 16 groups of 16

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
   int64_t cache_row = -1;  // the token's cache row of head 0
   if (a.slots) {
     const int slot = a.slots[tok], n_slots = a.cache.n_pages * a.cache.page_size;
-    if (slot >= n_slots) atomicExch(a.status, kStatusInvalid);
+    if (slot >= n_slots) atomicMax(a.status, kStatusInvalid);
     if (slot >= 0 && slot < n_slots)
       cache_row = (int64_t)(slot >> a.page_shift) * a.cache.Hkv * a.cache.page_size + (slot & (a.cache.page_size - 1));
   }
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int p
       for (int i = 0; i < U; ++i) {
         const int64_t r = r0 + i * step;
         const int slot = r < n ? slots[r] : -1;
-        if (slot >= n_slots) atomicExch(status, kStatusInvalid);
+        if (slot >= n_slots) atomicMax(status, kStatusInvalid);
         row[i] = slot < 0 || slot >= n_slots
                      ? -1
                      : ((int64_t)(slot >> page_shift) * c.Hkv + h) * c.page_size + (slot & (c.page_size - 1));
