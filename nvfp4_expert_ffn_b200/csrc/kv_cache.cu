@@ -11,10 +11,11 @@
 // side of a bf16 step, that on the other side of an E2M1 step, and the stored value is then off
 // by up to half of itself. Queries end in bf16 and are float32.
 //
-// Bound by HBM bytes for many tokens (per token: Hq + 2 Hkv rows of 2D bytes read, Hq rows
-// written, 9/16 byte per cached element), with the keys' float64 conversions (a quarter of the
-// rate of other float64 steps) next; for a decode step by launch latency and the float64 sine
-// and cosine.
+// Per token Hq + 2 Hkv rows of 2D bytes are read, Hq rows written, 9/16 byte a cached element: for
+// many tokens HBM's bytes would bound it, but the instructions do (issue slots 69% used). One B200:
+// norm and rotation of 16384 tokens (32 + 8 heads of 128) 80 us, 4.2 TB/s; with the write of keys
+// and values 27140 tokens 203 us, 3.6 TB/s. For a few tokens the launch and the float64 sine and
+// cosine: 4.1 us for 8 tokens (16 + 2 heads of 256), 7.4 us with the write.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
 // 8 elements a thread and output: 4 bytes of codes and the block's scale -> one 16-byte store
 // (bf16) or two (float32), of the key and the value at once. A thread keeps its head and place
 // and walks over the rows, four at a time, so that their loads are under way together. Bound by
-// the bytes written.
+// the bytes written: 65536 rows of 2 heads of 256 as bf16, 42 us (4.1 TB/s, launch included).
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int page_shift, const int32_t* __restrict__ slots,
                                                       int64_t n, void* __restrict__ k_out, void* __restrict__ v_out,
