@@ -404,7 +404,8 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes, which need no
  *   initialisation and may serve calls of any sizes up to those, one after the other; calls that
  *   may overlap need one each. The same call gives the same bits every time.
- * Limits: D and page_size as the cache, Hq <= 1024, n_seqs <= 65536, T * Hq < 2^31.
+ * Limits: D and page_size as the cache, Hq <= 1024, n_seqs <= 65536, T * Hq < 2^31,
+ * max_pages * page_size <= 2^30.
  */
 moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq, const int32_t* cu_q,
                               const int32_t* ctx_lens, const int32_t* block_table, int32_t n_seqs,

@@ -668,6 +668,7 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
 
 size_t nvfp4_kv_attention_workspace(int32_t T, int32_t n_seqs, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D) {
   if (T < 0 || n_seqs < 0 || max_q < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
+  if (Hq > 1024 || n_seqs > 65536 || (int64_t)T * Hq > 0x7fffffff) return 0;
   return kv_attn_ws(kMaxSms, T, n_seqs, max_q, Hq / Hkv, D).bytes;
 }
 
@@ -682,6 +683,8 @@ moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, in
   if (Hq < 1 || Hq % cache->Hkv) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "Hq must be a positive multiple of Hkv");
   if (Hq > 1024 || n_seqs > 65536 || (int64_t)T * Hq > 0x7fffffff)
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "at most 1024 heads, 65536 sequences and 2^31 - 1 query rows");
+  if ((int64_t)max_pages * cache->page_size > (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "a block table names at most 2^30 tokens a sequence");
   if (!(scale == scale)) return fail(MOE_ERR_INVALID_ARG, "scale is NaN");
   if (T == 0 || n_seqs == 0) return MOE_OK;
   if (max_q < 1) return fail(MOE_ERR_INVALID_ARG, "max_q must be the longest sequence's query tokens");

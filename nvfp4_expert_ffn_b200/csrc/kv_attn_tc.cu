@@ -1003,13 +1003,13 @@ __global__ void __launch_bounds__(Tc<D>::threads, 1) kv_attn_tc_kernel(const KvA
     sh.wait.abort = 0;
     sh.wait.limit = wait_limit_ns();
   }
+  MOE_PDL_PROLOGUE();
+  // (not before the wait: a block of an earlier kernel that has yet to allocate would wait for this one)
   if (warp == C::mma_warp) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  MOE_PDL_PROLOGUE();
-
   // ---- this block's run of the work
   Walk walk;
   walk.tiles = reinterpret_cast<const RowTile*>(a.tiles);

@@ -50,33 +50,34 @@ MOE_DEV float quotient(float x, float d, float y) {
 // Two lanes hold a block of 16 (8 elements each); amax is the block's, y the correctly rounded
 // 1 / ts. The scale and codes of quantize_block16 (common.cuh): E2M1 of the correctly rounded
 // x / denom. Blocks that the theorem does not cover are divided (an underflow on the way is none:
-// the result is 0 either way). The sign is x's own: that of a zero is lost on the way.
+// the result is 0 either way). The sign is x's own where the theorem is used: that of a zero is
+// lost on the way.
 MOE_DEV uint32_t quantize_half16(const uint4& p, float amax, float ts, float y, uint32_t* codes) {
   const bool good = good_divisor(ts) && amax < 0x1p60f;
   const float sb = good ? quotient(quotient(amax, kE2M1Max, 1.0f / kE2M1Max), ts, y) : __fdiv_rn(__fdiv_rn(amax, kE2M1Max), ts);
   const uint32_t s = f32_to_e4m3_sat(sb);
   *codes = 0;
-  if (s == 0) return s;
+  if ((s & 0x7Fu) == 0) return s;
   const float d = __fmul_rn(__half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(s))), ts);
   uint64_t v[4];
   unpack8x2(p, v);
-  float q[8];
-  if (good && good_divisor(d)) {
-    const float yd = __frcp_rn(d);
-    const uint64_t y2 = pack2(yd, yd), d2 = pack2(-d, -d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t q0 = mul2(v[i], y2);
-      unpack2(fma2(fma2(q0, d2, v[i]), y2, q0), q[2 * i], q[2 * i + 1]);
-    }
-  } else {
+  if (!good || !good_divisor(d)) {
+    const float denom = __fmul_rn(e4m3_to_f32(s), ts);  // (which takes the scale of a NaN for a number)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float lo, hi;
       unpack2(v[i], lo, hi);
-      q[2 * i] = __fdiv_rn(lo, d);
-      q[2 * i + 1] = __fdiv_rn(hi, d);
+      *codes |= f32x2_to_e2m1x2(__fdiv_rn(lo, denom), __fdiv_rn(hi, denom)) << (8 * i);
     }
+    return s;
+  }
+  float q[8];
+  const float yd = __frcp_rn(d);
+  const uint64_t y2 = pack2(yd, yd), d2 = pack2(-d, -d);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t q0 = mul2(v[i], y2);
+    unpack2(fma2(fma2(q0, d2, v[i]), y2, q0), q[2 * i], q[2 * i + 1]);
   }
   const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll

@@ -527,3 +527,23 @@ def test_many_tokens_match_few(D, Hq, Hkv, T):
     # two roundings to bf16 of values that differ by float32 roundings: at most a bf16 step
     assert np.all(np.abs(_np(qo) - _np(qs)) <= 2.0 ** -7 * np.maximum(np.abs(_np(qo)), np.abs(_np(qs))) + 2.0 ** -18)
     assert B.moe_get_device_status() == 0
+
+
+@pytest.mark.parametrize("ts", [0.0, 1e-38, 1e30, 3.0e38, 2.0 ** -61, 0.7, float("inf"), float("nan"), -0.02, -1e30])
+def test_append_quantises_as_the_quantiser_for_any_tensor_scale(ts):
+    """Tensor scales beyond the range of the fast quotients: the quantiser's bits, for rows of every
+    size, zeros, subnormals, infinities among them."""
+    rng = np.random.default_rng(16)
+    T, D = 300, 64
+    x = okv.to_bf16(rng.standard_normal((T, 1, D)) * np.exp2(rng.uniform(-130, 120, (T, 1, 1))))
+    x[::7, :, ::5] = 0.0
+    x[3, 0, 1], x[4, 0, 2], x[5] = np.inf, -np.inf, 0.0
+    v = _gpu(x).bfloat16()
+    t = torch.full((1,), ts, device=DEV)
+    cache = B.KVCache.allocate(-(-T // 16), 16, 1, D, t, t)
+    i32 = torch.arange(T, dtype=torch.int32, device=DEV)
+    B.nvfp4_kv_append(None, v, v, i32, i32, B.QKPrep(), cache, None)
+    codes, scales = torch.empty(T, D // 2, dtype=torch.uint8, device=DEV), torch.empty(T, D // 16, dtype=torch.uint8, device=DEV)
+    B.nvfp4_quantize_act(v.reshape(T, D), codes, scales, torch.empty(1, device=DEV), t)
+    for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert torch.equal(c.reshape(-1, D // 2)[:T], codes) and torch.equal(s.reshape(-1, D // 16)[:T], scales)

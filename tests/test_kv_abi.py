@@ -93,6 +93,15 @@ def test_attention_refusals():
     assert need(4, 2, 4, 5, 2, 128) == 0 and need(4, 2, 4, 4, 2, 96) == 0 and need(-1, 2, 4, 4, 2, 128) == 0
 
 
+def test_attention_sizes_past_the_limits():
+    """Key positions are 32-bit with room for a step past the end; the workspace size says so too."""
+    assert _attn(pages=(1 << 26) + 1, cache=_cache(page=16)) == SHAPE
+    assert _attn(pages=(1 << 20) + 1, cache=_cache(page=1024)) == SHAPE
+    need = B.lib().nvfp4_kv_attention_workspace
+    assert need(4, 65537, 4, 4, 2, 128) == 0 and need(4, 2, 4, 2048, 2, 128) == 0 and need(1 << 30, 2, 4, 4, 2, 128) == 0
+    assert need(1 << 20, 65536, 1 << 20, 1024, 8, 64) > 0
+
+
 def test_binding_checks_types_shapes_and_devices():
     u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
     c = B.KVCache(u8(3, 2, 16, 64), u8(3, 2, 16, 8), u8(3, 2, 16, 64), u8(3, 2, 16, 8), torch.ones(2), None)
