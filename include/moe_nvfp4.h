@@ -400,6 +400,9 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   outside cu_q[0] .. cu_q[n_seqs] are left as they were.
  *   Rows of a page number outside [0, n_pages) count as zeros, and set the device status to
  *   MOE_ERR_INVALID_ARG; cu_q (ascending) is read as clamped to [0, T] and ctx_lens to the table.
+ *   Rows that no sequence holds may contain anything. A scale of a held key or value that is NaN
+ *   (nvfp4_kv_append writes none for a finite tensor scale) can reach all queries of its sequence,
+ *   those before it too.
  *   The sums, maxima and outputs are float32, the softmax weights rounded to float16 and the
  *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes, which need no
  *   initialisation and may serve calls of any sizes up to those, one after the other; calls that

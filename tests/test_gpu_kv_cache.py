@@ -547,3 +547,50 @@ def test_append_quantises_as_the_quantiser_for_any_tensor_scale(ts):
     B.nvfp4_quantize_act(v.reshape(T, D), codes, scales, torch.empty(1, device=DEV), t)
     for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
         assert torch.equal(c.reshape(-1, D // 2)[:T], codes) and torch.equal(s.reshape(-1, D // 16)[:T], scales)
+
+
+@pytest.mark.parametrize("D,Hkv,G", [(128, 1, 64), (64, 1, 100), (256, 2, 33)])
+def test_attention_many_heads_on_one_key_head(D, Hkv, G):
+    """One token is more than 32 rows: single tokens through the kernel of many rows."""
+    Case(D, Hkv, G, 16, [1] * 5, [1, 17, 128, 129, 700], D + G).check()
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_attention_when_no_sequence_has_a_query(max_q):
+    c = Case(128, 1, 4, 16, [0, 0, 0], [30, 0, 200], 17, extra_rows=5)
+    out, lse = c.run(max_q=max_q)
+    assert torch.all(out == 3.0) and torch.all(lse == 3.0) and B.moe_get_device_status() == 0
+
+
+def test_attention_one_token_over_a_very_long_cache():
+    Case(64, 1, 1, 1024, [1, 1], [300001, 1], 18).check()
+
+
+def test_cache_of_more_than_four_gigabytes():
+    """Offsets past 32 bits: rows at the end of 2^22 + 64 tokens of 8 heads of 256."""
+    D, Hkv, page = 256, 8, 64
+    n_pages = (1 << 22) // page + 1
+    cache = B.KVCache.allocate(n_pages, page, Hkv, D)
+    assert cache.k_codes.numel() > 1 << 32
+    rng = np.random.default_rng(19)
+    T = 50
+    k, v, q = _bf16(rng, T, Hkv, D), _bf16(rng, T, Hkv, D), _bf16(rng, T, Hkv, D)
+    slots = ((n_pages - 1) * page + np.arange(T)).astype(np.int32)
+    kg, vg, qg = (_gpu(x).bfloat16() for x in (k, v, q))
+    B.nvfp4_kv_append(None, kg, vg, None, _gpu(slots), B.QKPrep(), cache, None)
+    oc = okv.Cache(1, page, Hkv, D)
+    for n, x in (("k", k), ("v", v)):
+        oc.write(n, x, np.arange(T))
+    out = [torch.empty(T, Hkv, D, device=DEV) for _ in range(2)]
+    B.nvfp4_kv_read(cache, _gpu(slots), *out)
+    kk, vv = oc.read("k", np.arange(T)), oc.read("v", np.arange(T))
+    assert np.array_equal(out[0].cpu().numpy(), kk) and np.array_equal(out[1].cpu().numpy(), vv)
+    assert not cache.k_codes[:T].any()  # where an offset cut to 32 bits would land
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    for n in (1, T):  # both kernels
+        o, e = torch.empty(n, Hkv, D, dtype=torch.bfloat16, device=DEV), torch.empty(n, Hkv, device=DEV)
+        ws = torch.empty(B.nvfp4_kv_attention_workspace(n, 1, n, Hkv, cache), dtype=torch.uint8, device=DEV)
+        B.nvfp4_kv_attention(qg[T - n:], i32(0, n), i32(T), i32(n_pages - 1)[None], n, cache, D ** -0.5, False, o, e, ws)
+        ref, lse, w, s = okv.attention(q[T - n:], kk, vv, D ** -0.5, False)
+        tol, tol_e = _attn_bounds(ref, w, s, lse, T, np.abs(vv).max(), D)
+        assert np.all(np.abs(_np(o) - ref) <= tol) and np.all(np.abs(e.cpu().numpy() - lse) <= tol_e)
