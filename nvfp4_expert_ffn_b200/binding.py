@@ -381,7 +381,7 @@ def _call(name: str, dev: int, stream, *args) -> None:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on device {dev}")
         s = stream.cuda_stream
     f = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = f(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -442,16 +442,16 @@ class QKPrep:
 
     _c: dict = field(default_factory=dict, repr=False, compare=False)
 
-    def struct(self, D: int, dev: int) -> _PrepC:
-        """The C structure for heads of D on GPU `dev`, built and checked once."""
-        c = self._c.get((D, dev))
-        if c is None:
+    def ref(self, D: int, dev: int):
+        """A reference to the C structure for heads of D on GPU `dev`, built and checked once."""
+        r = self._c.get((D, dev))
+        if r is None:
             f32 = torch.float32
             half = 0 if self.inv_freq is None else self.inv_freq.numel()
-            c = self._c[(D, dev)] = _PrepC(
+            r = self._c[(D, dev)] = ctypes.byref(_PrepC(
                 _need(self.q_weight, "q_weight", f32, (D,), dev), _need(self.k_weight, "k_weight", f32, (D,), dev), self.eps,
-                _need(self.inv_freq, "inv_freq", f32, (half,), dev), 2 * half, 1 if self.interleaved else 0, self.rot_scale)
-        return c
+                _need(self.inv_freq, "inv_freq", f32, (half,), dev), 2 * half, 1 if self.interleaved else 0, self.rot_scale))
+        return r
 
 
 def moe_qk_norm_rope(q, k, positions, prep: QKPrep, q_out, k_out, stream=None):
@@ -467,7 +467,7 @@ def moe_qk_norm_rope(q, k, positions, prep: QKPrep, q_out, k_out, stream=None):
     qo = None if q is None else _need(q_out, "q_out", q.dtype, (T, Hq, D), dev)
     ko = None if k is None else _need(k_out, "k_out", k.dtype, (T, Hkv, D), dev)
     pos = _need(positions, "positions", torch.int32, (T,), dev)
-    _call("moe_qk_norm_rope", dev, stream, qp, qs, kp, ks, T, Hq, Hkv, D, pos, ctypes.byref(prep.struct(D, dev)), qo, ko)
+    _call("moe_qk_norm_rope", dev, stream, qp, qs, kp, ks, T, Hq, Hkv, D, pos, prep.ref(D, dev), qo, ko)
 
 
 def nvfp4_kv_append(q, k, v, positions, slots, prep: QKPrep, cache: KVCache, q_out, stream=None):
@@ -483,7 +483,7 @@ def nvfp4_kv_append(q, k, v, positions, slots, prep: QKPrep, cache: KVCache, q_o
     vp, vs, _ = _head_rows(v, "v", T, D, dev)
     qo = None if q is None else _need(q_out, "q_out", q.dtype, (T, Hq, D), dev)
     pos, sl = _need(positions, "positions", i32, (T,), dev), _need(slots, "slots", i32, (T,), dev)
-    _call("nvfp4_kv_append", dev, stream, qp, qs, kp, ks, vp, vs, T, Hq, pos, sl, ctypes.byref(prep.struct(D, dev)), cache.ref, qo)
+    _call("nvfp4_kv_append", dev, stream, qp, qs, kp, ks, vp, vs, T, Hq, pos, sl, prep.ref(D, dev), cache.ref, qo)
 
 
 def nvfp4_kv_read(cache: KVCache, slots, k_out, v_out, stream=None):
