@@ -649,8 +649,11 @@ cudaError_t init_kv_attn_dec_attributes() {
 }
 
 cudaError_t launch_kv_attn_dec(const KvAttnArgs& a, int D, int num_sms, cudaStream_t st) {
-  // one group of 8 rows where every sequence fits it, else groups of 16
-  const bool one = (int64_t)a.max_q * a.G <= 8;
+  // Rows 8 at a time where every sequence fits that, and where the longer ones are the other kernel's
+  // and a single token fits it (beside a prompt, most of the rest are single tokens); else 16 at a
+  // time, at half the warps. 64 single tokens over 4096 keys beside a prompt of 512, 32 + 8 heads of
+  // 128: 125 us by 8, 162 by 16; 16 sequences of 4 tokens (16 rows) beside one: 88 and 80.
+  const bool one = a.G <= 8 && ((int64_t)a.max_q * a.G <= 8 || a.dec_max_rows < 0x7fffffff);
   if (D == 64) return one ? launch_dec<64, 1>(a, num_sms, st) : launch_dec<64, 2>(a, num_sms, st);
   if (D == 128) return one ? launch_dec<128, 1>(a, num_sms, st) : launch_dec<128, 2>(a, num_sms, st);
   return one ? launch_dec<256, 1>(a, num_sms, st) : launch_dec<256, 2>(a, num_sms, st);
