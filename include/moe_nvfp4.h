@@ -394,6 +394,7 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   cu_q[b] .. cu_q[b+1] - 1, none or more; max_q (host): the most that any sequence has.
  *   ctx_lens int32 [n_seqs]: its keys, its own queries' included when causal; block_table
  *   int32 [n_seqs][max_pages]: the pages that hold them, in order.
+ *   (A table no wider than the call's contexts lets short batches take fewer kernels.)
  *   Query i of n is at position ctx - n + i and sees the keys up to its own position (causal
  *   != 0) or all of them. out [T][Hq][D] bf16 = softmax(scale q k) v; lse float32 [T][Hq] (may
  *   be NULL) = log sum exp(scale q k). A query that sees no key gets 0 and -infinity. Tokens

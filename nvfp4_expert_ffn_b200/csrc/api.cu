@@ -700,6 +700,8 @@ moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, in
   max_q = max_q < T ? max_q : T;
   const KvAttnWs w = kv_attn_ws(sms, T, n_seqs, max_q, G, cache->D);
   if ((s = check_ws(ws, ws_bytes, w.bytes)) != MOE_OK) return s;
+  // (the block table's width is what the host knows of the context lengths)
+  const bool tc = w.tc && kv_attn_dec_units(T, n_seqs, G, cache->Hkv, cache->D, (int64_t)max_pages * cache->page_size) > kFewUnits;
   KvAttnArgs a = {};
   a.q = q;
   a.q_stride = q_stride;
@@ -725,10 +727,10 @@ moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, in
   a.partial = reinterpret_cast<float*>(base + w.partial);
   a.status = dstatus;
   for (a.page_shift = 0; (1 << a.page_shift) < cache->page_size;) ++a.page_shift;
-  a.dec_max_rows = w.tc ? kDecMaxRows : 0x7fffffff;
+  a.dec_max_rows = tc ? kDecMaxRows : 0x7fffffff;
   a.part_stride = kv_attn_dec_part_floats(cache->D);
   cudaError_t e = launch_kv_attn_dec(a, cache->D, sms, (cudaStream_t)stream);
-  if (e == cudaSuccess && w.tc) {
+  if (e == cudaSuccess && tc) {
     a.part_stride = kv_attn_tc_part_floats(cache->D);
     e = launch_kv_attn_tc(a, cache->D, sms, (cudaStream_t)stream);
   }

@@ -240,6 +240,13 @@ struct KvAttnArgs {
 // rows, tensor cores 116 to 121; 16 + 2 heads, D = 256: decode 46, 71, 95, 120, tensor cores 66
 // to 68. (One sequence of 1000 keys alone: decode 17 to 20 us up to 64 rows, tensor cores 31.)
 constexpr int kDecMaxRows = 32;
+// A batch whose work is no more than this many of the decode kernel's units (64 keys for 16 rows) is
+// left to it whole, two launches instead of five. 32 + 8 heads, D = 128, decode alone against both:
+// 736 units (16 tokens over 1000 keys) 20 and 32 us, 1920 26 and 33, 4400 32 and 37, 4608 38 and 31,
+// 5520 38 and 45, 7200 48 and 35, 11200 60 and 40. 16 + 2 heads of 256: 850 units 21 and 31 us, 3200
+// 34 and 37, 4256 46 and 68, 4608 32 and 35, 7040 58 and 47.
+constexpr int64_t kFewUnits = 4500;
+int64_t kv_attn_dec_units(int64_t T, int n_seqs, int G, int Hkv, int D, int64_t keys);  // at most
 size_t kv_attn_dec_part_floats(int D);
 size_t kv_attn_tc_part_floats(int D);
 int kv_attn_tc_max_tiles(int64_t T, int n_seqs, int G);

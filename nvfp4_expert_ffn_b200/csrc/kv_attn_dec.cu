@@ -639,6 +639,10 @@ cudaError_t attributes_dec() {
 
 size_t kv_attn_dec_part_floats(int D) { return 16 * (size_t)(D + 2); }
 
+int64_t kv_attn_dec_units(int64_t T, int n_seqs, int G, int Hkv, int D, int64_t keys) {
+  return (T * G / 16 + n_seqs) * Hkv * ((keys + kChunk - 1) / kChunk + start_chunks(D));
+}
+
 cudaError_t set_wait_limit_kv_attn_dec(unsigned long long ns) { return set_wait_limit_here(ns); }
 
 cudaError_t init_kv_attn_dec_attributes() {

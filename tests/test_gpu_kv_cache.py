@@ -181,7 +181,9 @@ class Case:
             self.cache.codes[n][:] = rng.integers(0, 256, self.cache.codes[n].shape)
             self.cache.scales[n][:] = 0x7F  # NaN
         order = rng.permutation(n_pages).astype(np.int32)
-        self.table = np.full((len(ctx), self.max_pages), 0x7ffffff0, np.int32)
+        # columns for 65536 keys: a table as wide as a server's, so that every kernel is used (narrow
+        # ones leave short batches to one kernel: check() runs both)
+        self.table = np.full((len(ctx), max(self.max_pages, 65536 // page)), 0x7ffffff0, np.int32)
         self.slots, at = [], 0
         for b, c in enumerate(ctx):
             self.table[b, :need[b]] = order[at:at + need[b]]
@@ -209,7 +211,15 @@ class Case:
         return out, e
 
     def check(self, causal=True, rows=None):
-        """Against the oracle; rows: at most that many query tokens of a sequence are checked."""
+        """Against the oracle, with the wide block table and one of the pages in use only; rows: at
+        most that many query tokens of a sequence are checked."""
+        wide = self.args
+        self._check(causal, rows)
+        self.args = wide[:2] + (wide[2][:, :self.max_pages].contiguous(),)
+        self._check(causal, rows)
+        self.args = wide
+
+    def _check(self, causal, rows):
         out, lse = self.run(causal)
         assert B.moe_get_device_status() == 0
         out, lse = _np(out), lse.cpu().numpy()
