@@ -1080,20 +1080,44 @@ __global__ void __launch_bounds__(256) kv_attn_tc_join_kernel(const KvAttnArgs a
   if (rr >= sq.n_q * a.G) return;
   const int first = blockIdx.x, last = meta.w;
   auto part = [&](int i) { return a.partial + ((size_t)i * 2 + (i == first ? 1 : 0)) * a.part_stride; };
-  constexpr int V = D / 64;  // float2 of a lane
+  constexpr int V = D / 64, N = 4;  // float2 of a lane
   float mm = kNoMax, ll = 0.0f;
   float2 acc[V] = {};
-  for (int i = first; i <= last; ++i) {
-    const float* p = part(i);
-    const float pm = p[row], top = fmaxf(mm, pm);
-    const float f0 = ex2(mm - top), f1 = ex2(pm - top);
+  // N parts' loads under way together: a few rows over a long context have many (74 for 16 tokens over
+  // 16000 keys, 69 us one by one, 63 so; eight at a time cost the usual two or three 3 us)
+  for (int i0 = first; i0 <= last; i0 += N) {
+    float pm[N], pl[N];
+    float2 v[N][V];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const bool some = i0 + k <= last;
+      const float* p = part(some ? i0 + k : last);
+      pm[k] = some ? p[row] : kNoMax;
+      pl[k] = some ? p[Tc<D>::rows + row] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        v[k][j] = some ? reinterpret_cast<const float2*>(p + 2 * Tc<D>::rows + row * D)[j * 32 + lane] : make_float2(0.0f, 0.0f);
+    }
+    float top = mm;
+#pragma unroll
+    for (int k = 0; k < N; ++k) top = fmaxf(top, pm[k]);
+    const float f0 = ex2(mm - top);
     mm = top;
-    ll = ll * f0 + p[Tc<D>::rows + row] * f1;
+    ll *= f0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float2 v = reinterpret_cast<const float2*>(p + 2 * Tc<D>::rows + row * D)[j * 32 + lane];
-      acc[j].x = acc[j].x * f0 + v.x * f1;
-      acc[j].y = acc[j].y * f0 + v.y * f1;
+      acc[j].x *= f0;
+      acc[j].y *= f0;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float f = ex2(pm[k] - top);
+      ll += pl[k] * f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        acc[j].x += v[k][j].x * f;
+        acc[j].y += v[k][j].y * f;
+      }
     }
   }
   const int tok = rr / a.G, head = meta.y * a.G + rr - tok * a.G;
