@@ -13,8 +13,8 @@
 //
 // Per token Hq + 2 Hkv rows of 2D bytes are read, Hq rows written, 9/16 byte a cached element: for
 // many tokens HBM's bytes would bound it, but the instructions do (issue slots 69% used). One B200:
-// norm and rotation of 16384 tokens (32 + 8 heads of 128) 80 us, 4.2 TB/s; with the write of keys
-// and values 27140 tokens 203 us, 3.6 TB/s. For a few tokens the launch and the float64 sine and
+// norm and rotation of 16384 tokens (32 + 8 heads of 128) 77 us, 4.3 TB/s; with the write of keys
+// and values, and those read back, 27140 tokens 200 us, 3.6 TB/s. For a few tokens the launch and the float64 sine and
 // cosine: 4.1 us for 8 tokens (16 + 2 heads of 256), 7.4 us with the write.
 #include <cuda_bf16.h>
 
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
 // 8 elements a thread and output: 4 bytes of codes and the block's scale -> one 16-byte store
 // (bf16) or two (float32), of the key and the value at once. A thread keeps its head and place
 // and walks over the rows, four at a time, so that their loads are under way together, and reads the
-// slots of the next four before (45 us without). Bound by
-// the bytes written: 65536 rows of 2 heads of 256 as bf16, 39 us (4.4 TB/s, launch included).
+// slots of the next four before (6 us less). Bound by
+// the bytes written: 65536 rows of 2 heads of 256 as bf16, 34 us (5.0 TB/s, launch included).
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int page_shift, const int32_t* __restrict__ slots,
                                                       int64_t n, void* __restrict__ k_out, void* __restrict__ v_out,
@@ -461,7 +461,7 @@ static cudaError_t launch_kv_read_d(const KvCacheArgs& c, const int32_t* slots, 
                                     int32_t* status, int num_sms, cudaStream_t st) {
   const int X = c.Hkv * (D / 8), per = X < 256 ? 256 / X : 1;
   // a block for every `per` rows while that is few; then as many as are resident, each of which walks,
-  // four rows at a time (8 a multiprocessor, in two waves: 41 us instead of 39)
+  // four rows at a time (8 a multiprocessor, in two waves, took 2 us more)
   const int64_t want = (n + per - 1) / per, most = (int64_t)num_sms * 4;
   const dim3 grid((unsigned)(want < most ? want : most)), block(256);
   int shift = 0;
