@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
   __shared__ __align__(16) uint4 s_q[RB * D / 8];
   __shared__ int s_e[RB];
   __shared__ float s_mm[RB], s_ll[RB];
-  __shared__ long long s_scan[W];
+  __shared__ long long s_scan[32];
   __shared__ long long s_local;
   __shared__ SeqSpan s_seq;
   __shared__ int s_b;
@@ -171,6 +171,11 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
     s_wait.limit = wait_limit_ns();
   }
   MOE_PDL_PROLOGUE();
+
+  if (a.dec_max_rows < 0x7fffffff && blockIdx.x == gridDim.x - 1) {
+    plan_tiles<THREADS, D>(a, s_scan);
+    __syncthreads();
+  }
 
   // ---- this block's run of chunks
   const int per = (a.n_seqs + THREADS - 1) / THREADS;

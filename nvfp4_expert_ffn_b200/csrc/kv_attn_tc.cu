@@ -28,8 +28,8 @@
 // instruction cache (an expander unrolled 16 times instead of 4 made the softmax 12% slower).
 //
 // Tiles have different numbers of keys (causal, ragged), so the work (key tiles, plus a few for
-// each row tile's start and end) is dealt to the blocks in equal contiguous runs; a plan kernel
-// writes the prefix sums, and row tiles that lie in more than one block are joined afterwards.
+// each row tile's start and end) is dealt to the blocks in equal contiguous runs by prefix sums
+// (plan_tiles), and row tiles that lie in more than one block are joined afterwards.
 #include <cuda_bf16.h>
 
 #include "kv_attn.cuh"
@@ -41,15 +41,14 @@ namespace {
 
 constexpr int kHalf = 128;  // rows of one M = 128 product
 constexpr int kSoftWarps = 8;
-constexpr int kPlanThreads = 1024;
 
 // The two forms. `pair`: two threads share a row of scores and a tile has 128 rows; otherwise a
 // thread has a row, and a tile 256 rows, half of them to each group of four softmax warps.
 template <int D>
 struct Tc {
   static constexpr bool pair = D == 256;
-  static constexpr int rows = pair ? kHalf : 2 * kHalf;  // of a tile
-  static constexpr int kt = pair ? 64 : 128;             // keys of a tile
+  static constexpr int rows = TileShape<D>::rows, kt = TileShape<D>::kt;
+  static_assert(rows == (pair ? kHalf : 2 * kHalf), "rows of a tile");
   static constexpr int exp_warps = pair ? 8 : 4;         // expanders, half of them for K
   static constexpr int mma_warp = kSoftWarps + exp_warps, load_warp = mma_warp + 2;
   static constexpr int threads = 32 * (kSoftWarps + exp_warps + 4);  // whole warpgroups
@@ -68,9 +67,6 @@ struct Tc {
   static constexpr int raw_bytes = kt * (D / 2 + D / 16);
   static constexpr int q_bytes = pair ? 0 : rows * D * 2;
   static constexpr int smem = q_bytes + 2 * stages * tile_bytes + raw_slots * raw_bytes + 1024;
-  // A row tile's start and end (its queries in, its rows out), in key tiles: 14500 cycles of 3400
-  // at D = 128, 19000 of 1800 at D = 256.
-  static constexpr int start_cost = pair ? 10 : 4;
 };
 
 struct TcShared {
@@ -83,96 +79,6 @@ struct TcShared {
   float x[2][kHalf];
   int e[2][kHalf];
 };
-
-// Row tiles of one key head, in order; a tile's share of the work starts at `start`.
-struct RowTile {
-  int b, tile, n_units, pad;
-  long long start;
-  long long pad2;
-};
-
-// keys that the tile's last row sees
-MOE_DEV int tile_keys(const KvAttnArgs& a, const SeqSpan& s, int tile, int tile_rows) {
-  if (!a.causal) return s.ctx;
-  const int last = min(s.n_q * a.G, (tile + 1) * tile_rows) - 1;
-  return min(s.ctx, max(s.ctx - s.n_q + last / a.G + 1, 0));
-}
-
-MOE_DEV int seq_tiles(const KvAttnArgs& a, const SeqSpan& s, int tile_rows) {
-  const int rows = s.n_q * a.G;
-  return rows > a.dec_max_rows ? (rows + tile_rows - 1) / tile_rows : 0;
-}
-
-// Exclusive block scan of one value per thread (kPlanThreads threads); *total the sum.
-MOE_DEV long long plan_scan(long long v, long long* tmp, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) tmp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = tmp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    tmp[lane] = w;
-  }
-  __syncthreads();
-  *total = tmp[31];
-  return (warp ? tmp[warp - 1] : 0) + x - v;
-}
-
-// One block: the list of row tiles and the prefix sums of their work.
-__global__ void __launch_bounds__(kPlanThreads) kv_attn_plan_kernel(const KvAttnArgs a, int tile_rows, int kt, int start_cost) {
-  MOE_PDL_PROLOGUE();
-  __shared__ long long tmp[32];
-  RowTile* tiles = reinterpret_cast<RowTile*>(a.tiles);
-  // 1. the tiles of every sequence, in order
-  long long at = 0;
-  for (int b0 = 0; b0 < a.n_seqs; b0 += kPlanThreads) {
-    const int b = b0 + threadIdx.x;
-    const int n = b < a.n_seqs ? seq_tiles(a, load_seq(a, b), tile_rows) : 0;
-    long long sum;
-    const long long first = at + plan_scan(n, tmp, &sum);
-    for (int i = 0; i < n && first + i < a.max_tiles; ++i) {
-      tiles[first + i].b = b;
-      tiles[first + i].tile = i;
-    }
-    at += sum;
-  }
-  __syncthreads();  // (and with it the writes above, for this block)
-  // more tiles than T rows can have: cu_q is not ascending
-  if (at > a.max_tiles && threadIdx.x == 0) atomicMax(a.status, kStatusInvalid);
-  const int n_tiles = (int)min(at, (long long)a.max_tiles);
-  // 2. their work
-  at = 0;
-  for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
-    const int i = i0 + threadIdx.x;
-    int units = 0;
-    if (i < n_tiles) {
-      const SeqSpan s = load_seq(a, tiles[i].b);
-      units = max(1, (tile_keys(a, s, tiles[i].tile, tile_rows) + kt - 1) / kt);
-    }
-    long long sum;
-    const long long start = at + plan_scan(i < n_tiles ? units + start_cost : 0, tmp, &sum);
-    if (i < n_tiles) {
-      tiles[i].n_units = units;
-      tiles[i].start = start;
-    }
-    at += sum;
-  }
-  if (threadIdx.x == 0) {
-    a.plan[0] = at;  // work of one key head
-    a.plan[1] = n_tiles;
-  }
-}
 
 // ---------------------------------------------------------------- TMEM helpers
 MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -1018,7 +924,7 @@ __global__ void __launch_bounds__(Tc<D>::threads, 1) kv_attn_tc_kernel(const KvA
   const long long total = walk.per_head * a.cache.Hkv;
   const int grid = (int)min((long long)gridDim.x, total);
   walk.at = walk.end = 0;
-  walk.start = C::start_cost;
+  walk.start = TileShape<D>::start_cost;
   if ((int)blockIdx.x < grid) {
     walk.at = total * blockIdx.x / grid;
     walk.end = total * (blockIdx.x + 1) / grid;
@@ -1133,9 +1039,7 @@ __global__ void __launch_bounds__(256) kv_attn_tc_join_kernel(const KvAttnArgs a
 template <int D>
 cudaError_t launch_tc(const KvAttnArgs& a, int num_sms, cudaStream_t st) {
   using C = Tc<D>;
-  cudaError_t e = launch_pdl(kv_attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, C::rows, C::kt, C::start_cost);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kv_attn_tc_kernel<D>, dim3(num_sms), dim3(C::threads), C::smem, st, a);
+  cudaError_t e = launch_pdl(kv_attn_tc_kernel<D>, dim3(num_sms), dim3(C::threads), C::smem, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_attn_tc_join_kernel<D>, dim3(num_sms, C::rows / 8), dim3(256), 0, st, a);
 }
