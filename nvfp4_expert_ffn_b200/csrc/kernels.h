@@ -235,16 +235,16 @@ struct KvAttnArgs {
 };
 
 // Query rows per key head up to which the decode kernel takes a sequence. It reads the cache again
-// for every 16 rows; the tensor-core kernel takes 128 as fast as 1, but starts 13 us later. 16
+// for every 16 rows; the tensor-core kernel takes 128 as fast as 1, but starts 10 us later. 16
 // sequences over 8192 keys, 32 + 8 heads, D = 128: decode 73, 126, 177, 229 us for 16, 32, 48, 64
 // rows, tensor cores 116 to 121; 16 + 2 heads, D = 256: decode 46, 71, 95, 120, tensor cores 66
-// to 68. (One sequence of 1000 keys alone: decode 17 to 20 us up to 64 rows, tensor cores 31.)
+// to 68. (One sequence of 1000 keys alone: decode 17 to 20 us up to 64 rows, tensor cores 29.)
 constexpr int kDecMaxRows = 32;
 // A batch whose work is no more than this many of the decode kernel's units (64 keys for 16 rows) is
-// left to it whole, two launches instead of five. 32 + 8 heads, D = 128, decode alone against both:
-// 736 units (16 tokens over 1000 keys) 20 and 32 us, 1920 26 and 33, 4400 32 and 37, 4608 38 and 31,
-// 5520 38 and 45, 7200 48 and 35, 11200 60 and 40. 16 + 2 heads of 256: 850 units 21 and 31 us, 3200
-// 34 and 37, 4256 46 and 68, 4608 32 and 35, 7040 58 and 47.
+// left to it whole, two launches instead of four. 32 + 8 heads, D = 128, decode alone against both:
+// 736 units (16 tokens over 1000 keys) 20 and 29 us, 1920 26 and 31, 4400 32 and 35, 5000 34 and 35,
+// 7200 48 and 33, 11200 60 and 38. 16 + 2 heads of 256: 850 units 22 and 29 us, 3200 34 and 35, 4256
+// 46 and 59, 4608 32 and 33, 7040 58 and 44.
 constexpr int64_t kFewUnits = 4500;
 int64_t kv_attn_dec_units(int64_t T, int n_seqs, int G, int Hkv, int D, int64_t keys);  // at most
 size_t kv_attn_dec_part_floats(int D);
