@@ -13,7 +13,7 @@
 //
 // Per token Hq + 2 Hkv rows of 2D bytes are read, Hq rows written, 9/16 byte a cached element: for
 // many tokens HBM's bytes would bound it, but the instructions do (issue slots 69% used). One B200:
-// norm and rotation of 16384 tokens (32 + 8 heads of 128) 77 us, 4.3 TB/s; with the write of keys
+// norm and rotation of 16384 tokens (32 + 8 heads of 128) 77 to 80 us, 4.3 TB/s; with the write of keys
 // and values, and those read back, 27140 tokens 200 us, 3.6 TB/s. For a few tokens the launch and the float64 sine and
 // cosine: 4.1 us for 8 tokens (16 + 2 heads of 256), 7.4 us with the write and the read back.
 #include <cuda_bf16.h>
