@@ -255,20 +255,21 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
 
   // ---- keys: stages of 32, dealt to the warps in turn
   constexpr int kStep = W * kStageKeys;
-  int t_issue = 0, page = -2;
+  int t_issue = 0, page = 0;
   auto tok_end_of = [](const Item& it) { return min(it.k1 * kChunk, it.sq.ctx); };
-  auto page_of = [&](const Item& it, int t) {  // of this lane's copy of the stage that starts at key t; read a stage early
-    t += part * rows_copy;
-    return lane < 8 && part < copies && t < tok_end_of(it)
-               ? __ldg(a.block_table + (int64_t)it.b * a.max_pages + (t >> a.page_shift))
-               : -2;
+  // Does this lane copy of the stage that starts at key t, and from which page: the number is read a
+  // stage early, and may be any.
+  const bool copier = lane < 8 && part < copies;
+  auto wanted_at = [&](const Item& it, int t) { return copier && t + part * rows_copy < tok_end_of(it); };
+  auto page_of = [&](const Item& it, int t) {
+    return wanted_at(it, t) ? __ldg(a.block_table + (int64_t)it.b * a.max_pages + ((t + part * rows_copy) >> a.page_shift)) : 0;
   };
   auto issue = [&](const Item& it) {
     const int next = page_of(it, t_issue + kStep);
     if (t_issue < tok_end_of(it)) {
       const uint32_t slot = n_issued++ % kStages;
-      const bool good = page >= 0 && page < a.cache.n_pages;
-      const uint32_t bads = __ballot_sync(0xffffffffu, page != -2 && !good), goods = __ballot_sync(0xffffffffu, good);
+      const bool wanted = wanted_at(it, t_issue), good = wanted && page >= 0 && page < a.cache.n_pages;
+      const uint32_t bads = __ballot_sync(0xffffffffu, wanted && !good), goods = __ballot_sync(0xffffffffu, good);
       if (lane == 0) {
         if (bads) atomicMax(a.status, kStatusInvalid);
         s_bad[warp][slot] = copies == 1 ? (bads ? 3u : 0u) : bads & 3u;
