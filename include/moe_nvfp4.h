@@ -404,8 +404,9 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   Rows that no sequence holds may contain anything. A scale of a held key or value that is NaN
  *   (nvfp4_kv_append writes none for a finite tensor scale) can reach all queries of its sequence,
  *   those before it too.
- *   The sums, maxima and outputs are float32, the softmax weights rounded to float16 and the
- *   cached values exact. ws: nvfp4_kv_attention_workspace(...) bytes, which need no
+ *   The sums, maxima and outputs are float32, the cached values exact, and the softmax weights
+ *   rounded to float16: by 2^-11 of themselves, or by 2^-32 of the query's largest weight where
+ *   that is more. ws: nvfp4_kv_attention_workspace(...) bytes, which need no
  *   initialisation and may serve calls of any sizes up to those, one after the other; calls that
  *   may overlap need one each. The same call gives the same bits every time.
  * Limits: D and page_size as the cache, Hq <= 1024, n_seqs <= 65536, T * Hq < 2^31,

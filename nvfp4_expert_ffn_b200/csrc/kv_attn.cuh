@@ -11,8 +11,13 @@ namespace moe {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A running maximum is raised only when a score passes it by this much (in powers of two):
-// the weights then stay below 2^8, far inside float16, and most tiles rescale nothing.
+// Weights are 2^(score - m), held in float16, with a reference m that follows the running maximum:
+// it is set kLead below a maximum, and again only when a weight passes 2^(kLead + kRaise), so that
+// most tiles rescale nothing. Weights so reach up to 2^15, half of float16's largest, and a key whose
+// weight is 2^-21 of the largest or more keeps all 11 bits; below that it is off by 2^-32 of the largest
+// at most. (With the largest at 2^0, long contexts beside one dominant key lost their tail: it
+// counted in the float32 sum, but in the products weights below 2^-25 were zero.)
+constexpr float kLead = 7.0f;
 constexpr float kRaise = 8.0f;
 constexpr float kNoMax = -3.402823466e38f;  // no key seen yet
 

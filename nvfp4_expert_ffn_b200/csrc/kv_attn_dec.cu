@@ -22,7 +22,7 @@
 // 8192 keys, 32 + 8 heads of 128, 99 us (3.7 TB/s); 8 sequences near 16384 keys, 16 + 2 heads of
 // 256, 30 us; one over 1000 keys 12.7 us.
 // q is scaled by a power of two per row into float16's range (exact; the factor returns in
-// the softmax scale), the weights P are rounded to float16 (11 bits; the result is bf16, 8),
+// the softmax scale), the weights P are rounded to float16 (11 bits; the result is bf16, 8; see kLead),
 // sums, maxima and the output stay in float32.
 //
 // The keys of all sequences and heads are cut into chunks of kChunk and dealt to the blocks in
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
             if (edge && t0 + key_of(g) + 8 * (j >> 1) >= lim[r][j & 1]) s[r][j] = -INFINITY;
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) raise |= fmaxf(s[r][j], s[r][j + 2]) > m[r][j] + kRaise;
+          for (int j = 0; j < 2; ++j) raise |= fmaxf(s[r][j], s[r][j + 2]) - m[r][j] > kLead + kRaise;
         }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
               float x = fmaxf(s[r][j], s[r][j + 2]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-              x = fmaxf(x, m[r][j]);
+              x = fmaxf(x - kLead, m[r][j]);
               fix[j] = ex2(m[r][j] - x);
               m[r][j] = x;
               l[r][j] *= fix[j];

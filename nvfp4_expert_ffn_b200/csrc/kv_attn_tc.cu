@@ -13,7 +13,7 @@
 //     A operand in TMEM, float16 too.
 //   softmax warps: they copy S to registers first, so the next Q K^T can overwrite it while they
 //     work. O is rescaled only when a row's maximum rises by more than 2^8 over the one in use;
-//     the weights are below 2^8 in float16, the sums in float32.
+//     the weights are below 2^15 in float16 (kLead), the sums in float32.
 // D <= 128: two groups of 128 rows, a softmax thread to a row, KT = 128. The groups share the
 //   expanded keys, which are a third of a softmax's instructions again, and S; O of both, S and
 //   both P fill TMEM, so Q is in shared memory. Bound by the softmax warps' instructions and the
@@ -329,13 +329,13 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
         mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
       // the two warps of these 32 rows decide together
-      if (bar_or(1 + quarter, 64, mx > m + kRaise || !ok)) {
+      if (bar_or(1 + quarter, 64, mx - m > kLead + kRaise || !ok)) {
         sh.x[half][row] = mx;
         if (bar_or(1 + quarter, 64, !ok)) {
           ok = false;
           break;
         }
-        const float top = fmaxf(fmaxf(sh.x[0][row], sh.x[1][row]), m);
+        const float top = fmaxf(fmaxf(sh.x[0][row], sh.x[1][row]) - kLead, m);
         if (u > run.u0) {
           const float fix = ex2(m - top);
           float a0, a1;
@@ -535,8 +535,8 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       for (int i = 0; i < KT; i += 2)
         mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
-      if (__any_sync(0xffffffffu, mx > m + kRaise)) {
-        const float top = fmaxf(mx, m);
+      if (__any_sync(0xffffffffu, mx - m > kLead + kRaise)) {
+        const float top = fmaxf(mx - kLead, m);
         if (j > 0) {
           const float fix = ex2(m - top);
           float a0, a1;
