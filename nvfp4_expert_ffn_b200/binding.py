@@ -440,7 +440,8 @@ class QKPrep:
     interleaved: bool = False
     rot_scale: float = 1.0
 
-    _c: dict = field(default_factory=dict, repr=False, compare=False)
+    # C structures by (D, device); each object's own, dataclasses.replace makes an empty one
+    _c: dict = field(init=False, default_factory=dict, repr=False, compare=False)
 
     def ref(self, D: int, dev: int):
         """A reference to the C structure for heads of D on GPU `dev`, built and checked once."""
