@@ -62,7 +62,12 @@ struct Tc {
   static constexpr uint32_t q_col = D, s_col = pair ? q_col + D / 2 : 2 * D, p_col = s_col + kt;
   static_assert(p_col + kt <= 512, "TMEM columns");
   static constexpr int stages = 2;                       // expanded tiles of K, and of V
-  static constexpr int raw_slots = D == 128 ? 3 : 8;     // raw tiles, K and V in turn
+  // Raw tiles, K and V in turn. Copies may land in any order, and a wait for a parity is over while
+  // the barrier is still in the phase before, so the expanders of K and of V must each have barriers
+  // of their own: with an odd number of slots, whose fills take turns, twice as many as slots.
+  static constexpr int raw_slots = D == 128 ? 3 : 8;
+  static constexpr int raw_bars = raw_slots % 2 ? 2 * raw_slots : raw_slots;
+  static_assert(raw_bars % 2 == 0 && raw_bars <= 8, "barriers of the raw tiles");
   static constexpr int tile_bytes = kt * D * 2;
   static constexpr int raw_bytes = kt * (D / 2 + D / 16);
   static constexpr int q_bytes = pair ? 0 : rows * D * 2;
@@ -647,7 +652,7 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
 // two 16-byte stores, lanes that would meet in a bank take the second one first.
 template <int D>
 MOE_DEV void expand(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_k, uint8_t* s_v, uint8_t* s_raw) {
-  constexpr int KT = Tc<D>::kt, NS = Tc<D>::stages, RAW = Tc<D>::raw_slots;
+  constexpr int KT = Tc<D>::kt, NS = Tc<D>::stages, RAW = Tc<D>::raw_slots, BARS = Tc<D>::raw_bars;
   constexpr int EW = Tc<D>::exp_warps / 2;  // expander warps of K, and of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int P = D / 16;                 // lanes of a row
@@ -670,7 +675,7 @@ MOE_DEV void expand(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_k,
 #pragma unroll 1
     for (int u = run.u0; u < run.u1; ++u, ++tc) {
       const uint32_t n_raw = 2 * tc + (is_v ? 1 : 0), slot = n_raw % RAW, s = tc % NS;
-      ok = wait_both(&sh.raw_full[slot], (n_raw / RAW) & 1, &empty[s], ((tc / NS) & 1) ^ 1, &sh.wait, a.status);
+      ok = wait_both(&sh.raw_full[n_raw % BARS], (n_raw / BARS) & 1, &empty[s], ((tc / NS) & 1) ^ 1, &sh.wait, a.status);
       if (!ok) break;
       const uint8_t* raw = s_raw + slot * Tc<D>::raw_bytes;
       const uint32_t bad = sh.bad[slot];
@@ -718,7 +723,7 @@ MOE_DEV void expand(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_k,
 // ---------------------------------------------------------------- loader
 template <int D>
 MOE_DEV void load_raw(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_raw) {
-  constexpr int KT = Tc<D>::kt, RAW = Tc<D>::raw_slots;
+  constexpr int KT = Tc<D>::kt, RAW = Tc<D>::raw_slots, BARS = Tc<D>::raw_bars;
   const int lane = threadIdx.x & 31;
   // a lane copies one page's part of the tile: at most KT / 16 pages
   uint32_t n_raw = 0;
@@ -751,17 +756,18 @@ MOE_DEV void load_raw(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_
         const uint32_t slot = n_raw % RAW;
         ok = __all_sync(0xffffffffu, wait_soon(&sh.raw_empty[slot], ((n_raw / RAW) & 1) ^ 1, &sh.wait, a.status));
         if (!ok) break;
+        uint64_t* landed = &sh.raw_full[n_raw % BARS];
         uint8_t* raw = s_raw + slot * Tc<D>::raw_bytes;
         if (lane == 0) {
           sh.bad[slot] = bad;
-          mbar_arrive_expect_tx(&sh.raw_full[slot], __popc(goods) * rows * (D / 2 + D / 16));
+          mbar_arrive_expect_tx(landed, __popc(goods) * rows * (D / 2 + D / 16));
         }
         __syncwarp();
         if (good) {
           bulk_g2s(raw + lane * rows * (D / 2), (i ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2), rows * (D / 2),
-                   &sh.raw_full[slot]);
+                   landed);
           bulk_g2s(raw + KT * (D / 2) + lane * rows * (D / 16), (i ? a.cache.v_scales : a.cache.k_scales) + row * (D / 16),
-                   rows * (D / 16), &sh.raw_full[slot]);
+                   rows * (D / 16), landed);
         }
       }
       page = next;
@@ -771,7 +777,7 @@ MOE_DEV void load_raw(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_
   __syncwarp();
   for (uint32_t j = n_raw > RAW ? n_raw - RAW : 0; j < n_raw; ++j) {
     volatile int no_abort = 0;
-    mbar_wait(&sh.raw_full[j % RAW], (j / RAW) & 1, &no_abort, a.status);
+    mbar_wait(&sh.raw_full[j % BARS], (j / BARS) & 1, &no_abort, a.status);
   }
 }
 
@@ -893,10 +899,8 @@ __global__ void __launch_bounds__(Tc<D>::threads, 1) kv_attn_tc_kernel(const KvA
       mbar_init(&sh.v_full[s], EW);
       mbar_init(&sh.v_empty[s], 1);
     }
-    for (int i = 0; i < C::raw_slots; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], EW);
-    }
+    for (int i = 0; i < C::raw_bars; ++i) mbar_init(&sh.raw_full[i], 1);
+    for (int i = 0; i < C::raw_slots; ++i) mbar_init(&sh.raw_empty[i], EW);
     mbar_init(&sh.s_empty, soft);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], soft);

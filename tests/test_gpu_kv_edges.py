@@ -70,3 +70,21 @@ def test_many_small_weights_beside_a_dominant_one(D, Hkv, G, n, gap):
     out, lse = c.run(causal=False)
     assert np.all(np.abs(_np(out) - ref) <= tol), (np.abs(_np(out) - ref) / ref).max()
     assert np.all(np.abs(lse.cpu().numpy() - e) <= dS + ctx * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(e)))
+
+
+# ---------------------------------------------------------------- copies that land in another order
+
+@pytest.mark.parametrize("D,G,n,ctx", [(128, 4, 40, 20011), (128, 4, 25, 40000), (64, 3, 100, 20011), (256, 4, 40, 20011)])
+def test_a_split_context_gives_the_same_bits_whatever_lies_in_the_caches(D, G, n, ctx):
+    """Blocks of one to four key tiles, started on keys that are in L2 and on keys that a large write has
+    driven out of it, so that a block's first copies land late and in any order."""
+    c = Case(D, 1, G, 64, [n], [ctx], D + n)
+    q = _gpu(c.q).bfloat16()
+    want, lse = c.run(q=q)
+    sweep = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(60):
+        if i % 2:
+            sweep.fill_(i)
+        out, e = c.run(q=q)
+        assert torch.equal(out, want) and torch.equal(e, lse), i
+    assert B.moe_get_device_status() == 0
