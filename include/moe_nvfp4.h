@@ -341,6 +341,8 @@ typedef struct moe_kv_cache {
  *   rot_scale           factor on sine and cosine (1 unless the frequency scaling has one)
  * Keys are computed in float64 and rounded to float32 and then to bf16; queries in float32 with
  * the sines and cosines from float64 angles.
+ * Infinities and NaN give what the formulas give: a NaN, or an infinity that meets a zero or
+ * an infinity of the other sign, is NaN; a norm makes zeros of the numbers beside an infinity.
  */
 typedef struct moe_qk_prep {
   const float* q_weight;

@@ -136,6 +136,7 @@ MOE_DEV double widen(uint32_t w, int high) {
   const uint32_t hi = high ? ((w & 0x7FFF0000u) >> 3) | (w & 0x80000000u) : ((w & 0x7FFFu) << 13) | ((w & 0x8000u) << 16);
   return __hiloint2double((int)hi, 0);
 }
+MOE_DEV double bf16_to_f64(uint32_t w, int high) { return (double)__uint_as_float(high ? w & 0xFFFF0000u : w << 16); }
 
 // Calls body(row's 16 bytes, head, live) for the heads first + sub, first + step + sub, ... of a
 // token, PF rows' loads under way: one row at a time leaves most of the memory's latency
@@ -268,19 +269,38 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
   // ---- keys, in float64
   if (a.Hk) each_row<2>(a.k + tok * a.k_stride, a.Hk, first(0), sub, step, D, e0, [&](uint4 p, int h, bool live) {
     const uint4 pp = hop ? partner(p) : beside(p);
-    if (a.k_weight || turned) {
+    uint32_t m = __vmaxu2(__vmaxu2(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu), __vmaxu2(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu));
+    if (__any_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16) >= 0x7F80u)) {
+      // infinities or NaN in one of the warp's rows (which hold the partners too): the same, converted as
+      // what they are, in short code
+      auto element = [](const uint4& w, int i) { return bf16_to_f64(i & 4 ? (i & 2 ? w.w : w.z) : (i & 2 ? w.y : w.x), i & 1); };
+      double rs = 1.0;
+      if (a.k_weight) {
+        double ss = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) ss = fma(element(p, i), element(p, i), ss);
+#pragma unroll 1
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        rs = norm_factor(ss, D, a.eps);
+      }
+      if (a.k_weight || turned) {
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          double z = element(p, i) * s_ka[t][i * L + lane];
+          if (turned) z = fma(element(pp, i) * (1.0 / kUp), s_kb[t][i * L + lane], z);
+          // in at the top of y, the others 16 bits down
+          y = make_uint4(__funnelshift_r(y.x, y.y, 16), __funnelshift_r(y.y, y.z, 16), __funnelshift_r(y.z, y.w, 16),
+                         __funnelshift_r(y.w, pack_bf16((float)(z * rs), 0.0f), 16));
+        }
+        p = y;
+      }
+    } else if (a.k_weight || turned) {
       uint32_t x[4] = {p.x, p.y, p.z, p.w};
       const uint32_t xp[4] = {pp.x, pp.y, pp.z, pp.w};
       double v[8], rs = 1.0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = widen(x[i >> 1], i & 1) * kUp;
-      uint32_t m = __vmaxu2(__vmaxu2(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu), __vmaxu2(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu));
-      const bool special = max(m & 0xFFFFu, m >> 16) >= 0x7F80u;
-      if (special) {  // (an infinity counts as the NaN that the norm or the rotation makes of it)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (((x[i >> 1] >> (16 * (i & 1))) & 0x7F80u) == 0x7F80u) v[i] = __longlong_as_double(0x7FF8000000000000ll);
-      }
       if (a.k_weight) {
         double ss = 0.0;
 #pragma unroll

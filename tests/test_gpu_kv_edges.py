@@ -1,5 +1,6 @@
 """The cache and attention calls at values and indices that ordinary data does not have: page
-numbers that a kernel might take for a mark of its own, weights far below the largest."""
+numbers that a kernel might take for a mark of its own, weights far below the largest, infinities
+and NaN in queries and keys."""
 import numpy as np
 import pytest
 import torch
@@ -9,6 +10,8 @@ from nvfp4_expert_ffn_b200 import binding as B
 from test_gpu_kv_cache import Case, _attn_bounds, _bf16, _gpu, _np
 
 pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
 
 
 # ---------------------------------------------------------------- page numbers
@@ -87,4 +90,56 @@ def test_a_split_context_gives_the_same_bits_whatever_lies_in_the_caches(D, G, n
             sweep.fill_(i)
         out, e = c.run(q=q)
         assert torch.equal(out, want) and torch.equal(e, lse), i
+    assert B.moe_get_device_status() == 0
+
+
+# ---------------------------------------------------------------- keys and queries that are not finite
+
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (64, 64, True), (128, 32, False), (128, 96, True), (256, 0, False)])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("T", [6, 700])
+def test_infinities_and_nan_in_queries_and_keys(D, rot, inter, norm, T):
+    """Where the formula gives NaN or an infinity so do both, and where it gives a number so do they:
+    through a rotation without a norm an element that is not finite reaches its partner, through a
+    norm an infinity makes zeros of its row's numbers and NaN makes all of it NaN."""
+    rng = np.random.default_rng(D + rot + T)
+    x = _bf16(rng, T, 5, D)
+    odd = np.array([np.inf, -np.inf, np.nan, 3.0e38, -1e-39], np.float32)
+    for h in range(1, 5):  # (head 0 stays ordinary)
+        for _ in range(h - 1 or 1):
+            x[np.arange(T), h, rng.integers(0, D, T)] = odd[rng.integers(0, 5, T)]
+    x[::3, 4, 0], x[::3, 4, 1], x[1::3, 4, rot // 2] = np.inf, -np.inf, np.nan
+    x = _np(_gpu(x).bfloat16())
+    pos = rng.integers(0, 1 << 17, T).astype(np.int32)
+    pos[::4] = 0
+    f = (1e4 ** (-np.arange(rot // 2) / max(rot // 2, 1))).astype(np.float32)
+    w = rng.uniform(0.5, 1.5, D).astype(np.float32) if norm else None
+    wg = None if w is None else _gpu(w)
+    prep = B.QKPrep(wg, wg, 1e-6, _gpu(f) if rot else None, inter, 1.0)
+    xg = _gpu(x).bfloat16()
+    bits = xg.view(torch.int16)
+    bits[1::2][torch.isnan(xg[1::2])] = -63  # 0xFFC1: NaN with its sign set
+    qo, ko = torch.empty_like(xg), torch.empty_like(xg)
+    B.moe_qk_norm_rope(xg, xg, _gpu(pos), prep, qo, ko)
+    with np.errstate(all="ignore"):
+        ref = okv.norm_rope(x, pos, w, 1e-6, f if rot else None, inter, 1.0)
+        fin = np.isfinite(ref) & (np.abs(ref) < 3.38e38)  # (the largest numbers may round up to an infinity)
+        rms = np.where(np.isfinite(x), np.abs(x), 0).astype(np.float64).max(axis=-1, keepdims=True)
+        pair = 2.0 ** -24 * (D / 16 + 16) * np.sqrt(2) * 1.5 * (np.sqrt(D) if norm else rms)  # as in test_norm_rope
+        for got, err in ((qo, pair), (ko, 0.0)):
+            got = _np(got).astype(np.float64)
+            assert np.array_equal(np.isnan(got), np.isnan(ref))
+            inf = np.isinf(ref)
+            assert np.array_equal(got[inf], ref[inf]) and not np.isinf(got[np.isfinite(ref) & fin]).any()
+            assert np.all((np.abs(got - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -23) + err + 1e-37)[fin])
+    # and what the cache then holds is the quantiser's
+    cache = B.KVCache.allocate(-(-T // 16), 16, 5, D)
+    slots = torch.arange(T, dtype=torch.int32, device=DEV)
+    B.nvfp4_kv_append(None, xg, xg, _gpu(pos), slots, prep, cache, None)
+    for src, codes, scales in ((ko, cache.k_codes, cache.k_scales), (xg, cache.v_codes, cache.v_scales)):
+        qc, qs = torch.empty(T * 5, D // 2, dtype=torch.uint8, device=DEV), torch.empty(T * 5, D // 16, dtype=torch.uint8, device=DEV)
+        B.nvfp4_quantize_act(src.reshape(T * 5, D), qc, qs, torch.empty(1, device=DEV), torch.ones(1, device=DEV))
+        for got, want in ((codes, qc), (scales, qs)):
+            got = got.transpose(1, 2).reshape(-1, 5, got.shape[-1])[:T].reshape(T * 5, -1)
+            assert torch.equal(got, want)
     assert B.moe_get_device_status() == 0
