@@ -382,7 +382,7 @@ moe_status nvfp4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* 
 /*
  * nvfp4_kv_read - cached rows back as numbers: k_out, v_out [n][Hkv][D] (either may be NULL),
  * bf16 or float32 by out_type (MOE_TYPE_*): (e2m1 * e4m3) * ts in float32, rounded once more
- * for bf16. slots int32 [n], repeats allowed; a negative slot gives zeros, one past the end
+ * for bf16; a scale of 0x7F or 0xFF is E4M3's NaN. slots int32 [n], repeats allowed; a negative slot gives zeros, one past the end
  * too, and sets the device status to MOE_ERR_INVALID_ARG.
  */
 moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int64_t n, int32_t out_type,

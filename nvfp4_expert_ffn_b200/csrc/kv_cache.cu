@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int p
         for (int i = 0; i < U; ++i) {
           const int64_t r = r0 + i * step;
           if (r >= n) break;
-          const float sc = row[i] < 0 ? 0.0f : e4m3_to_f32(s[side][i]);
+          const float sc = row[i] < 0 ? 0.0f : __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(s[side][i])));  // (0x7F and 0xFF are NaN)
           uint32_t f[4];
           e2m1x8_to_f16x2x4(row[i] < 0 ? 0u : w[side][i], f);
           float v[8];

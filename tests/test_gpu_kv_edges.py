@@ -1,11 +1,12 @@
 """The cache and attention calls at values and indices that ordinary data does not have: page
 numbers that a kernel might take for a mark of its own, weights far below the largest, infinities
-and NaN in queries and keys."""
+and NaN in queries, keys and scales."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import kv as okv
+from oracle import nvfp4 as onv
 from nvfp4_expert_ffn_b200 import binding as B
 from test_gpu_kv_cache import Case, _attn_bounds, _bf16, _gpu, _np
 
@@ -143,3 +144,29 @@ def test_infinities_and_nan_in_queries_and_keys(D, rot, inter, norm, T):
             got = got.transpose(1, 2).reshape(-1, 5, got.shape[-1])[:T].reshape(T * 5, -1)
             assert torch.equal(got, want)
     assert B.moe_get_device_status() == 0
+
+
+# ---------------------------------------------------------------- scales that are NaN
+
+def test_a_scale_that_is_nan_reads_as_nan():
+    """E4M3's 0x7F and 0xFF are NaN for the reader as they are for attention; a negative scale is a
+    negative number."""
+    cache = B.KVCache.allocate(1, 16, 2, 64)
+    rng = np.random.default_rng(0)
+    for t in (cache.k_codes, cache.v_codes):
+        t.copy_(_gpu(rng.integers(0, 256, tuple(t.shape)).astype(np.uint8)))
+    scales = rng.integers(0, 256, tuple(cache.k_scales.shape)).astype(np.uint8)
+    scales.reshape(-1)[:4] = 0x7F, 0xFF, 0x7E, 0xFE
+    cache.k_scales.copy_(_gpu(scales))
+    cache.v_scales.copy_(_gpu(scales[:, :, ::-1].copy()))
+    slots = torch.tensor(list(range(16)) + [-1], dtype=torch.int32, device=DEV)
+    for dtype, eps in ((torch.float32, 0.0), (torch.bfloat16, 2.0 ** -8)):
+        ko, vo = (torch.empty(17, 2, 64, dtype=dtype, device=DEV) for _ in range(2))
+        B.nvfp4_kv_read(cache, slots, ko, vo)
+        for got, codes, sc in ((ko, cache.k_codes, cache.k_scales), (vo, cache.v_codes, cache.v_scales)):
+            ref = np.stack([onv.dequantize(codes[0, h].cpu().numpy(), sc[0, h].cpu().numpy(), 1.0) for h in range(2)], 1)
+            assert np.isnan(ref).any()
+            got = _np(got)
+            assert np.array_equal(np.isnan(got[:16]), np.isnan(ref)) and not got[16].any()
+            ok = ~np.isnan(ref)
+            assert np.all(np.abs(got[:16][ok] - ref[ok]) <= np.abs(ref[ok]) * eps)
