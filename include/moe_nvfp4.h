@@ -382,8 +382,8 @@ moe_status nvfp4_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* 
 /*
  * nvfp4_kv_read - cached rows back as numbers: k_out, v_out [n][Hkv][D] (either may be NULL),
  * bf16 or float32 by out_type (MOE_TYPE_*): (e2m1 * e4m3) * ts in float32, rounded once more
- * for bf16; a scale of 0x7F or 0xFF is E4M3's NaN. slots int32 [n], repeats allowed; a negative slot gives zeros, one past the end
- * too, and sets the device status to MOE_ERR_INVALID_ARG.
+ * for bf16; a scale of 0x7F or 0xFF is E4M3's NaN. slots int32 [n], repeats allowed; a negative
+ * slot gives zeros, one past the end too, and sets the device status to MOE_ERR_INVALID_ARG.
  */
 moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int64_t n, int32_t out_type,
                          void* k_out, void* v_out, void* stream);
@@ -403,6 +403,8 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   outside cu_q[0] .. cu_q[n_seqs] are left as they were.
  *   Rows of a page number outside [0, n_pages) count as zeros, and set the device status to
  *   MOE_ERR_INVALID_ARG; cu_q (ascending) is read as clamped to [0, T] and ctx_lens to the table.
+ *   A tensor scale k_ts, or a scale, that is NaN or infinite makes NaN of the head's queries that
+ *   see a key.
  *   Rows that no sequence holds may contain anything. A scale of a held key or value that is NaN
  *   (nvfp4_kv_append writes none for a finite tensor scale) can reach all queries of its sequence,
  *   those before it too.

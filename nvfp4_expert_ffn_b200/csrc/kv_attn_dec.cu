@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
     uint32_t bq[NR][KSTEPS][2];
     float fac[NR][2];
     int lim[NR][2], lim_min = 0x7fffffff;
-    const float kts = a.cache.k_ts ? a.cache.k_ts[h] : 1.0f;
+    const float ks = score_scale(a, h);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
 #pragma unroll
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int ej = s_e[8 * r + 2 * c + j];
-        fac[r][j] = a.scale * kLog2e * kts * __int_as_float((127 - 13 + ej) << 23);
+        fac[r][j] = ks * __int_as_float((127 - 13 + ej) << 23);
         const int rj = row_first + 8 * r + 2 * c + j;
         // keys that row may see: all of the context, or up to its own position
         lim[r][j] = rj >= rows ? 0 : a.causal ? max(it.sq.ctx - it.sq.n_q + rj / a.G + 1, 0) : it.sq.ctx;

@@ -184,6 +184,13 @@ MOE_DEV bool wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_
   return __all_sync(0xffffffffu, wait_soon(odd ? bar1 : bar0, odd ? parity1 : parity0, w, status));
 }
 
+// The factor of a row's scores, 2^(e - 13) of the head's. Never zero, so that a masked score stays
+// -infinity; NaN only for a row that sees a key, for the same reason.
+MOE_DEV float row_factor(float ks, int e, int keys) {
+  const float f = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
+  return ks != ks && keys > 0 ? ks : f;
+}
+
 // A run of key tiles of one row tile.
 struct Run {
   int b, h, tile, u0, u1, n_units;
@@ -262,7 +269,8 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
     const int rows = sq.n_q * a.G, rr = run.tile * kHalf + row;
     const bool live = rr < rows;
     const int tok = live ? rr / a.G : 0, head = run.h * a.G + (live ? rr - tok * a.G : 0);
-    const float ks = a.scale * (a.cache.k_ts ? a.cache.k_ts[run.h] : 1.0f) * kLog2e;
+    const float ks = score_scale(a, run.h);
+    const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
     // ---- Q: this thread's half of the row
     float fac;
     {
@@ -283,7 +291,7 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       const int e = max(max(sh.e[0][row], sh.e[1][row]), -100);
       // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
       const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
-      fac = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
+      fac = row_factor(ks, e, lim);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         uint32_t f[16];
@@ -301,7 +309,6 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[0]);
     }
-    const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
     // keys that every row of the tile sees
     const int first_tok = run.tile * kHalf / a.G;
     const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
@@ -479,7 +486,8 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
     float m = kNoMax;
     uint64_t l2 = pack2(0.0f, 0.0f);
     float fac;
-    const float ks = a.scale * (a.cache.k_ts ? a.cache.k_ts[run.h] : 1.0f) * kLog2e;
+    const float ks = score_scale(a, run.h);
+    const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
     // ---- Q, float16 scaled by a power of two, K-major in the 128-byte swizzle
     {
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(sq.q0 + tok) * a.q_stride + (int64_t)head * D);
@@ -496,7 +504,7 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       const int e = max((int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127, -100);
       // the row's largest element becomes 2^13..2^14; a negative scale turns its sign here
       const float up = copysignf(__int_as_float((127 + 13 - e) << 23), ks);
-      fac = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
+      fac = row_factor(ks, e, lim);
       uint8_t* dst = s_q + g * (kHalf * D * 2) + row * 128;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
@@ -513,7 +521,6 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[g]);
     }
-    const int lim = !live ? 0x7fffffff : a.causal ? max(sq.ctx - sq.n_q + tok + 1, 0) : sq.ctx;
     // keys that every row of this half sees
     const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_row / a.G + 1, 0) : sq.ctx;
     const uint64_t fac2 = pack2(fac, fac);

@@ -170,3 +170,33 @@ def test_a_scale_that_is_nan_reads_as_nan():
             assert np.array_equal(np.isnan(got[:16]), np.isnan(ref)) and not got[16].any()
             ok = ~np.isnan(ref)
             assert np.all(np.abs(got[:16][ok] - ref[ok]) <= np.abs(ref[ok]) * eps)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [2, 70])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_tensor_scales_that_are_not_finite_reach_every_query_that_sees_a_key(D, n, bad):
+    """A NaN or infinite scale of a head's keys makes that head's rows NaN in both kernels (infinities of
+    both signs are among an infinite key's products), one of its values leaves nothing finite in them;
+    rows that see no key stay at 0 and -infinity, and the other head as it was."""
+    c = Case(D, 2, 4, 16, [n, n], [60, n - 1], 31)
+    want, lse0 = c.run()
+    ts = {"k": c.gcache.k_ts, "v": c.gcache.v_ts}
+    g = c.gcache
+    for name in "kv":
+        t = dict(ts)
+        t[name] = t[name].clone()
+        t[name][1] = bad
+        c.gcache = B.KVCache(g.k_codes, g.k_scales, g.v_codes, g.v_scales, t["k"], t["v"])
+        out, lse = c.run()
+        assert torch.equal(out[:, :4], want[:, :4]) and torch.equal(lse[:, :4], lse0[:, :4])
+        none = torch.isneginf(lse0[:, 4:])  # queries before the first key
+        assert none[n].all() and int(none.sum()) == 4 * (1 + max(0, n - 60))
+        assert not out[:, 4:][none].any() and torch.isneginf(lse[:, 4:][none]).all()
+        seen = out[:, 4:][~none]
+        if name == "k":
+            assert torch.isnan(seen).all() and torch.isnan(lse[:, 4:][~none]).all()
+        else:
+            assert not torch.isfinite(seen).any() and torch.equal(lse, lse0)
+            assert torch.isnan(seen).all() or bad == float("inf")
+    assert B.moe_get_device_status() == 0
