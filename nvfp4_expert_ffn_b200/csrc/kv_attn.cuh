@@ -20,7 +20,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLead = 7.0f;
 constexpr float kRaise = 8.0f;
 constexpr float kNoMax = -3.402823466e38f;  // no key seen yet
-
 MOE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -191,6 +191,12 @@ MOE_DEV float row_factor(float ks, int e, int keys) {
   return ks != ks && keys > 0 ? ks : f;
 }
 
+// Can a row of the warp have scores (s * fac, with |s| up to D times 2^14 times 6 * 448) past 2^22? There
+// one fused step s * fac - m can leave a weight outside float16's range, because m is a rounded product:
+// the products are then rounded first.
+template <int D>
+MOE_DEV bool scores_far(float fac) { return __any_sync(0xffffffffu, fac * (D * 16384.0f * 2688.0f) > 0x1p22f); }
+
 // A run of key tiles of one row tile.
 struct Run {
   int b, h, tile, u0, u1, n_units;
@@ -314,7 +320,8 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
     const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
     float m = kNoMax;
     uint64_t l2 = pack2(0.0f, 0.0f);
-    const uint64_t fac2 = pack2(fac, fac);
+    const bool far = scores_far<D>(fac);
+    const uint64_t fac2 = far ? pack2(1.0f, 1.0f) : pack2(fac, fac);
     for (int u = run.u0; u < run.u1; ++u, ++tc) {
       // the scores, and the product that last read this tile's columns of P
       if (tc >= 2)
@@ -370,6 +377,15 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
         }
         m = top;
         bar_or(1 + quarter, 64, false);  // s_x is free again
+      }
+      if (__builtin_expect(far, 0)) {
+#pragma unroll
+        for (int i = 0; i < HK; i += 2) {
+          float x0, x1;
+          unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(fac, fac)), x0, x1);
+          s[i] = __float_as_uint(x0);
+          s[i + 1] = __float_as_uint(x1);
+        }
       }
       const uint64_t nm2 = pack2(-m, -m);
       const uint32_t tp = tl + C::p_col + (tc & 1) * (KT / 2) + half * (HK / 2);
@@ -523,7 +539,8 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
     }
     // keys that every row of this half sees
     const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_row / a.G + 1, 0) : sq.ctx;
-    const uint64_t fac2 = pack2(fac, fac);
+    const bool far = scores_far<D>(fac);
+    const uint64_t fac2 = far ? pack2(1.0f, 1.0f) : pack2(fac, fac);
     for (int j = 0; j < n; ++j, ++tc) {
       ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[g], tc & 1, &sh.wait, a.status));
       if (!ok) break;
@@ -569,6 +586,15 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
           tmem_st_wait();
         }
         m = top;
+      }
+      if (__builtin_expect(far, 0)) {
+#pragma unroll
+        for (int i = 0; i < KT; i += 2) {
+          float x0, x1;
+          unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(fac, fac)), x0, x1);
+          s[i] = __float_as_uint(x0);
+          s[i + 1] = __float_as_uint(x1);
+        }
       }
       const uint64_t nm2 = pack2(-m, -m);
 #pragma unroll

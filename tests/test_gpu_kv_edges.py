@@ -1,6 +1,6 @@
 """The cache and attention calls at values and indices that ordinary data does not have: page
 numbers that a kernel might take for a mark of its own, weights far below the largest, infinities
-and NaN in queries, keys and scales."""
+and NaN in queries, keys and scales, scores of any size."""
 import numpy as np
 import pytest
 import torch
@@ -199,4 +199,34 @@ def test_tensor_scales_that_are_not_finite_reach_every_query_that_sees_a_key(D, 
         else:
             assert not torch.isfinite(seen).any() and torch.equal(lse, lse0)
             assert torch.isnan(seen).all() or bad == float("inf")
+    assert B.moe_get_device_status() == 0
+
+
+# ---------------------------------------------------------------- scores of any size
+
+@pytest.mark.parametrize("D,Hkv,G", [(64, 1, 2), (128, 2, 4), (256, 1, 3)])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 22, 2.0 ** 26, 2.0 ** 29, 2.0 ** 40, 2.0 ** 90])
+def test_scores_far_past_one_give_the_largest_keys_value(D, Hkv, G, n, size):
+    """Scores up to 10^27: where the first key leads the second by more than the scores' float32
+    error, the output is its value, rounded to bf16 after a weight rounded to float16; the others weigh
+    e^-60 at most."""
+    c = Case(D, Hkv, G, 16, [n, n], [300, 65], D + n, qscale=size)
+    out, lse = c.run(causal=False)
+    out, lse = _np(out), lse.cpu().numpy()
+    clear = 0
+    for b in range(2):
+        k, v = c.cache.read("k", c.slots[b]), c.cache.read("v", c.slots[b])
+        for t in range(c.cu[b], c.cu[b + 1]):
+            for h in range(c.Hq):
+                s = D ** -0.5 * (k[:, h // G] @ c.q[t, h].astype(np.float64))
+                logit = D ** -0.5 * (np.abs(k[:, h // G]) @ np.abs(c.q[t, h].astype(np.float64))).max()
+                dS = logit * (D * 2.0 ** -23 + 2.0 ** -21) + 2.0 ** -21
+                assert np.isfinite(out[t, h]).all() and abs(lse[t, h] - s.max()) <= dS + 2.0 ** -22 * abs(s.max()) + np.log(len(k))
+                first, second = np.sort(s)[:-3:-1]
+                if first - second > 2 * dS + 60:
+                    clear += 1
+                    top = v[s.argmax(), h // G]
+                    assert np.all(np.abs(out[t, h] - top) <= np.abs(top) * (2.0 ** -8 + 2.0 ** -10) + len(k) * np.exp(-60.0) * np.abs(v).max())
+    assert clear >= 0.8 * 2 * n * c.Hq
     assert B.moe_get_device_status() == 0
