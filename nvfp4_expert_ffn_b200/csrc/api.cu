@@ -33,12 +33,13 @@ struct DeviceInfo {
   bool ready = false;
   int num_sms = 0;
   int32_t* status = nullptr;  // device address of g_device_status on this device
+  cudaError_t kv_attn_tc = cudaSuccess;  // may the attention kernel of many query rows run?
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
 // Per-device one-time setup: SM count and dynamic shared memory limits.
-moe_status device_info(int* num_sms, int32_t** status = nullptr) {
+moe_status device_info(int* num_sms, int32_t** status = nullptr, cudaError_t* kv_attn_tc = nullptr) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -54,7 +55,7 @@ moe_status device_info(int* num_sms, int32_t** status = nullptr) {
                                     std::to_string(major * 10 + minor));
     e = cudaDeviceGetAttribute(&di.num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-    e = init_kernel_attributes();
+    e = init_kernel_attributes(&di.kv_attn_tc);
     if (e != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
     e = cudaGetSymbolAddress(reinterpret_cast<void**>(&di.status), g_device_status);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(g_device_status)");
@@ -62,6 +63,7 @@ moe_status device_info(int* num_sms, int32_t** status = nullptr) {
   }
   *num_sms = di.num_sms;
   if (status) *status = di.status;
+  if (kv_attn_tc) *kv_attn_tc = di.kv_attn_tc;
   return MOE_OK;
 }
 
@@ -695,13 +697,15 @@ moe_status nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int32_t T, in
   if (!aligned16(out)) return fail(MOE_ERR_INVALID_ARG, "out must be 16-byte aligned");
   int sms = 0;
   int32_t* dstatus = nullptr;
-  if ((s = device_info(&sms, &dstatus)) != MOE_OK) return s;
+  cudaError_t tc_usable = cudaSuccess;
+  if ((s = device_info(&sms, &dstatus, &tc_usable)) != MOE_OK) return s;
   const int G = Hq / cache->Hkv;
   max_q = max_q < T ? max_q : T;
   const KvAttnWs w = kv_attn_ws(sms, T, n_seqs, max_q, G, cache->D);
   if ((s = check_ws(ws, ws_bytes, w.bytes)) != MOE_OK) return s;
   // (the block table's width is what the host knows of the context lengths)
   const bool tc = w.tc && kv_attn_dec_units(T, n_seqs, G, cache->Hkv, cache->D, (int64_t)max_pages * cache->page_size) > kFewUnits;
+  if (tc && tc_usable != cudaSuccess) return cuda_fail(tc_usable, "nvfp4_kv_attention: the kernel of many query rows cannot run");
   KvAttnArgs a = {};
   a.q = q;
   a.q_stride = q_stride;

@@ -282,7 +282,9 @@ cudaError_t init_ffn_decode_attributes();
 cudaError_t init_ffn_tc_attributes();
 cudaError_t init_ffn_dec_attributes();
 cudaError_t init_layer_dec_attributes();
-inline cudaError_t init_kernel_attributes() {
+// The attention kernel of many query rows has a condition of its own (its roles' registers): *kv_attn_tc
+// says whether it may run, which no other call needs to know.
+inline cudaError_t init_kernel_attributes(cudaError_t* kv_attn_tc) {
   cudaError_t e = init_route_attributes();
   if (e != cudaSuccess) return e;
   e = init_router_tc_attributes();
@@ -295,8 +297,7 @@ inline cudaError_t init_kernel_attributes() {
   if (e != cudaSuccess) return e;
   e = init_kv_attn_dec_attributes();
   if (e != cudaSuccess) return e;
-  e = init_kv_attn_tc_attributes();
-  if (e != cudaSuccess) return e;
+  *kv_attn_tc = init_kv_attn_tc_attributes();
   return init_layer_dec_attributes();
 }
 
