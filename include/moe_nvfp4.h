@@ -403,6 +403,8 @@ moe_status nvfp4_kv_read(const moe_kv_cache_t* cache, const int32_t* slots, int6
  *   outside cu_q[0] .. cu_q[n_seqs] are left as they were.
  *   Rows of a page number outside [0, n_pages) count as zeros, and set the device status to
  *   MOE_ERR_INVALID_ARG; cu_q (ascending) is read as clamped to [0, T] and ctx_lens to the table.
+ *   Offsets that go back and so name more rows than T have set it too where they pass what the
+ *   workspace lists; nothing outside the arrays is touched, but out and lse are then not valid.
  *   A tensor scale k_ts, or a scale, that is NaN or infinite makes NaN of the head's queries that
  *   see a key.
  *   Rows that no sequence holds may contain anything. A scale of a held key or value that is NaN

@@ -230,3 +230,29 @@ def test_scores_far_past_one_give_the_largest_keys_value(D, Hkv, G, n, size):
                     assert np.all(np.abs(out[t, h] - top) <= np.abs(top) * (2.0 ** -8 + 2.0 ** -10) + len(k) * np.exp(-60.0) * np.abs(v).max())
     assert clear >= 0.8 * 2 * n * c.Hq
     assert B.moe_get_device_status() == 0
+
+
+# ---------------------------------------------------------------- offsets that do not ascend
+
+def test_offsets_that_go_back_are_reported_and_stay_inside_the_workspace():
+    """Offsets that name the same 2000 tokens 40 times make 1280 tiles of rows, nine times what a
+    workspace of 2000 tokens lists: the rest is left out, the status says so, and what lies behind
+    the workspace and the next call's results are as they were."""
+    T, page = 2000, 16
+    c = Case(64, 1, 4, page, [T], [T], 41)
+    seqs = 80
+    need = B.nvfp4_kv_attention_workspace(T, seqs, T, c.Hq, c.gcache)
+    buf = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    c.ws = buf[:need]
+    good, lse = c.run()
+    assert B.moe_get_device_status() == 0
+    args = c.args
+    c.args = (torch.tensor([0, T] * 40 + [0], dtype=torch.int32, device=DEV),
+              torch.full((seqs,), 16, dtype=torch.int32, device=DEV), args[2].repeat(seqs, 1))
+    c.run()
+    assert B.moe_get_device_status() == B.MOE_ERR_INVALID_ARG
+    assert torch.all(buf[need:] == 0xA5)
+    c.args = args
+    again, lse2 = c.run()
+    assert B.moe_get_device_status() == 0
+    assert torch.equal(again, good) and torch.equal(lse2, lse)
