@@ -256,3 +256,23 @@ def test_offsets_that_go_back_are_reported_and_stay_inside_the_workspace():
     again, lse2 = c.run()
     assert B.moe_get_device_status() == 0
     assert torch.equal(again, good) and torch.equal(lse2, lse)
+
+
+# ---------------------------------------------------------------- the smoke run
+
+def test_the_smoke_run_launches_both_attention_kernels_and_both_writers(tmp_path):
+    import json
+
+    import __graft_entry__ as entry
+    from torch.profiler import ProfilerActivity, profile
+    with profile(activities=[ProfilerActivity.CUDA]) as p:
+        assert entry._smoke_attention(DEV) <= 5e-3
+        torch.cuda.synchronize()
+    p.export_chrome_trace(str(tmp_path / "trace.json"))
+    runs = {(e["name"].split("<")[0].split("::")[-1], e["args"]["block"][0])
+            for e in json.loads((tmp_path / "trace.json").read_text())["traceEvents"] if e.get("cat") == "kernel"}
+    names = {n for n, _ in runs}
+    for kernel in ("kv_attn_tc_kernel", "kv_attn_tc_join_kernel", "kv_attn_dec_kernel", "kv_attn_join_kernel"):
+        assert kernel in names, runs
+    # the writer of few tokens has blocks of eight warps, that of many blocks of four
+    assert {b for n, b in runs if n == "qkv_prep_kernel"} == {128, 256}, runs
