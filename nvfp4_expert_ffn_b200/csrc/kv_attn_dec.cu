@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
   const bool copier = lane < 8 && part < copies;
   auto wanted_at = [&](const Item& it, int t) { return copier && t + part * rows_copy < tok_end_of(it); };
   auto page_of = [&](const Item& it, int t) {
-    return wanted_at(it, t) ? __ldg(a.block_table + (int64_t)it.b * a.max_pages + ((t + part * rows_copy) >> a.page_shift)) : 0;
+    return wanted_at(it, t) ? a.block_table[(int64_t)it.b * a.max_pages + ((t + part * rows_copy) >> a.page_shift)] : 0;
   };
   auto issue = [&](const Item& it) {
     const int next = page_of(it, t_issue + kStep);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(32 * dec_warps(D, NR), dec_blocks(D, NR)) kv_a
       const int r = i / QL, piece = i % QL, row = row_first + r;
       const bool live = row < rows && r < RB;
       const int tok = live ? row / a.G : 0, head = h * a.G + (live ? row - tok * a.G : 0);
-      const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(it.sq.q0 + tok) * a.q_stride + (int64_t)head * D) + piece)
+      const uint4 raw = live ? reinterpret_cast<const uint4*>(a.q + (int64_t)(it.sq.q0 + tok) * a.q_stride + (int64_t)head * D)[piece]
                              : make_uint4(0u, 0u, 0u, 0u);
       const uint32_t m2 = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu), __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
       int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7) - 127;

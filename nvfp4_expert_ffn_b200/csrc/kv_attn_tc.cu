@@ -286,7 +286,7 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        raw[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
         mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
         mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
@@ -511,7 +511,7 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
       uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        raw[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         mx = __vmaxu2(mx, raw[i].x & 0x7FFF7FFFu);
         mx = __vmaxu2(mx, raw[i].y & 0x7FFF7FFFu);
         mx = __vmaxu2(mx, raw[i].z & 0x7FFF7FFFu);
@@ -770,7 +770,7 @@ MOE_DEV void load_raw(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint8_t* s_
     const int32_t* table = a.block_table + (int64_t)run.b * a.max_pages;
     auto page_of = [&](int u) {
       const int t = u * KT + lane * rows;
-      return lane < copies && t < ctx ? __ldg(table + (t >> a.page_shift)) : 0;
+      return lane < copies && t < ctx ? table[t >> a.page_shift] : 0;
     };
     int page = page_of(run.u0);
     for (int u = run.u0; u < run.u1 && ok; ++u) {

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
       m = __float_as_uint(fmaxf(top, __shfl_xor_sync(3u << (wl & ~1), top, 1))) >> 16;
     }
     if (!live || cache_row < 0) return;
-    const float ts = tsp ? __ldg(tsp + h) : 1.0f;
+    const float ts = tsp ? tsp[h] : 1.0f;
     uint32_t c;
     const uint32_t s = quantize_half16(p, bf16_to_f32(m), ts, __frcp_rn(ts), &c);
     const int64_t row = cache_row + (int64_t)h * a.cache.page_size;
@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
 // slots of the next four before (6 us less). Bound by
 // the bytes written: 65536 rows of 2 heads of 256 as bf16, 34 us (5.0 TB/s, launch included).
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int page_shift, const int32_t* __restrict__ slots,
-                                                      int64_t n, void* __restrict__ k_out, void* __restrict__ v_out,
+__global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int page_shift, const int32_t* slots,
+                                                      int64_t n, void* k_out, void* v_out,
                                                       int32_t* status) {
   MOE_PDL_PROLOGUE();
   constexpr int L = D / 8, U = 4;

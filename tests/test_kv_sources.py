@@ -1,0 +1,19 @@
+"""What the cache's and attention's kernels must not do, checked in their source (CPU only)."""
+import glob
+import os
+import re
+
+import pytest
+
+from nvfp4_expert_ffn_b200 import binding as B
+
+SRC = sorted(glob.glob(os.path.join(os.path.dirname(os.path.abspath(B.__file__)), "csrc", "kv_*")))
+
+
+@pytest.mark.parametrize("path", SRC, ids=os.path.basename)
+def test_no_loads_through_the_read_only_path(path):
+    """These kernels start while the one before may still write their inputs (queries, slots, page
+    numbers), so those are not read-only for a kernel's whole life, which __ldg and a pointer that is
+    const and __restrict__ would promise."""
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    assert "__ldg" not in text and "__restrict__" not in text and not re.search(r"ld\.global[.\w]*\.nc", text)
