@@ -181,7 +181,9 @@ MOE_DEV float max3(float a, float b, float c) {
 // still costs the round trip). For a whole warp; the same answer in all lanes.
 MOE_DEV bool wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1, Patience* w, int32_t* status) {
   const bool odd = threadIdx.x & 1;
-  return __all_sync(0xffffffffu, wait_soon(odd ? bar1 : bar0, odd ? parity1 : parity0, w, status));
+  const bool ok = __all_sync(0xffffffffu, wait_soon(odd ? bar1 : bar0, odd ? parity1 : parity0, w, status));
+  __syncwarp();  // what a barrier has made visible to the lanes that waited for it holds for the others (a vote orders no memory)
+  return ok;
 }
 
 // The factor of a row's scores, 2^(e - 13) of the head's. Never zero, so that a masked score stays

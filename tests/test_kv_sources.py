@@ -17,3 +17,11 @@ def test_no_loads_through_the_read_only_path(path):
     const and __restrict__ would promise."""
     text = re.sub(r"//[^\n]*", "", open(path).read())
     assert "__ldg" not in text and "__restrict__" not in text and not re.search(r"ld\.global[.\w]*\.nc", text)
+
+
+def test_a_wait_shared_out_over_a_warp_ends_with_a_warp_barrier():
+    """Half of the lanes wait for one barrier, half for another: what each makes visible reaches the other
+    half by the warp barrier behind the vote, which orders no memory itself."""
+    text = open([p for p in SRC if p.endswith("kv_attn_tc.cu")][0]).read()
+    body = re.search(r"MOE_DEV bool wait_both\(.*?\n}\n", text, re.S).group(0)
+    assert body.index("wait_soon(") < body.index("__syncwarp()") < body.index("return ok;")
