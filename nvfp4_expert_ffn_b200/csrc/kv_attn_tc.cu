@@ -187,10 +187,11 @@ MOE_DEV bool wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_
 }
 
 // The factor of a row's scores, 2^(e - 13) of the head's. Never zero, so that a masked score stays
-// -infinity; NaN only for a row that sees a key, for the same reason.
+// -infinity; NaN only for a row that sees a key, for the same reason. (In arithmetic, as the kernel of
+// few rows has it, it cost 0.6% here, by the registers.)
 MOE_DEV float row_factor(float ks, int e, int keys) {
   const float f = fmaxf(fabsf(ks) * __int_as_float((127 - 13 + e) << 23), 1.2e-38f);
-  return ks != ks && keys > 0 ? ks : f;
+  return !(fabsf(ks) < INFINITY) && keys > 0 ? __int_as_float(0x7fffffff) : f;
 }
 
 // Can a row of the warp have scores (s * fac, with |s| up to D times 2^14 times 6 * 448) past 2^22? There
