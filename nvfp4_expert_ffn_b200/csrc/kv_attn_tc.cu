@@ -32,6 +32,8 @@
 // (plan_tiles), and row tiles that lie in more than one block are joined afterwards.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "kv_attn.cuh"
 #include "sm100.cuh"
 
@@ -323,95 +325,96 @@ MOE_DEV void softmax_pair(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
     const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_tok + 1, 0) : sq.ctx;
     float m = kNoMax;
     uint64_t l2 = pack2(0.0f, 0.0f);
-    const bool far = scores_far<D>(fac);
-    const uint64_t fac2 = far ? pack2(1.0f, 1.0f) : pack2(fac, fac);
-    for (int u = run.u0; u < run.u1; ++u, ++tc) {
-      // the scores, and the product that last read this tile's columns of P
-      if (tc >= 2)
-        ok = wait_both(&sh.s_full[0], tc & 1, &sh.pv_done[tc & 1], ((tc >> 1) - 1) & 1, &sh.wait, a.status) && ok;
-      else
-        ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[0], tc & 1, &sh.wait, a.status)) && ok;
-      tc_fence_after();
-      uint32_t s[HK];
+    const uint64_t fac2 = pack2(fac, fac);
+    auto keys = [&](auto rounded) {  // (two loops: a choice in one cost 1%)
+      for (int u = run.u0; u < run.u1; ++u, ++tc) {
+        // the scores, and the product that last read this tile's columns of P
+        if (tc >= 2)
+          ok = wait_both(&sh.s_full[0], tc & 1, &sh.pv_done[tc & 1], ((tc >> 1) - 1) & 1, &sh.wait, a.status) && ok;
+        else
+          ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[0], tc & 1, &sh.wait, a.status)) && ok;
+        tc_fence_after();
+        uint32_t s[HK];
 #pragma unroll
-      for (int i = 0; i < HK; i += 32) tmem_ld32(tl + C::s_col + half * HK + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_empty);
-      if (u * KT + KT > lim_min) {
-        const int left = lim - u * KT - half * HK;
+        for (int i = 0; i < HK; i += 32) tmem_ld32(tl + C::s_col + half * HK + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_empty);
+        if (u * KT + KT > lim_min) {
+          const int left = lim - u * KT - half * HK;
 #pragma unroll
-        for (int i = 0; i < HK; ++i)
-          if (i >= left) s[i] = 0xff800000u;
-      }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < HK; i += 2)
-        mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
-      // the two warps of these 32 rows decide together
-      if (bar_or(1 + quarter, 64, mx - m > kLead + kRaise || !ok)) {
-        sh.x[half][row] = mx;
-        if (bar_or(1 + quarter, 64, !ok)) {
-          ok = false;
-          break;
+          for (int i = 0; i < HK; ++i)
+            if (i >= left) s[i] = 0xff800000u;
         }
-        const float top = fmaxf(fmaxf(sh.x[0][row], sh.x[1][row]) - kLead, m);
-        if (u > run.u0) {
-          const float fix = ex2(m - top);
-          float a0, a1;
-          unpack2(l2, a0, a1);
-          l2 = pack2(a0 * fix, a1 * fix);
-          ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &sh.wait, a.status));
-          tc_fence_after();
-          if (ok) {
-#pragma unroll 1
-            for (int c = 0; c < D / 2; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tl + half * (D / 2) + c, o);
-              tmem_ld_wait();
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-              tmem_st32(tl + half * (D / 2) + c, o);
-            }
-            tmem_st_wait();
+        for (int i = 0; i < HK; i += 2)
+          mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
+        // the two warps of these 32 rows decide together
+        if (bar_or(1 + quarter, 64, mx - m > kLead + kRaise || !ok)) {
+          sh.x[half][row] = mx;
+          if (bar_or(1 + quarter, 64, !ok)) {
+            ok = false;
+            break;
           }
-        }
-        m = top;
-        bar_or(1 + quarter, 64, false);  // s_x is free again
-      }
-      if (__builtin_expect(far, 0)) {
+          const float top = fmaxf(fmaxf(sh.x[0][row], sh.x[1][row]) - kLead, m);
+          if (u > run.u0) {
+            const float fix = ex2(m - top);
+            float a0, a1;
+            unpack2(l2, a0, a1);
+            l2 = pack2(a0 * fix, a1 * fix);
+            ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, &sh.wait, a.status));
+            tc_fence_after();
+            if (ok) {
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tl + half * (D / 2) + c, o);
+                tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < HK; i += 2) {
-          float x0, x1;
-          unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(fac, fac)), x0, x1);
-          s[i] = __float_as_uint(x0);
-          s[i + 1] = __float_as_uint(x1);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+                tmem_st32(tl + half * (D / 2) + c, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          m = top;
+          bar_or(1 + quarter, 64, false);  // s_x is free again
         }
-      }
-      const uint64_t nm2 = pack2(-m, -m);
-      const uint32_t tp = tl + C::p_col + (tc & 1) * (KT / 2) + half * (HK / 2);
+        const uint64_t nm2 = pack2(-m, -m);
+        const uint32_t tp = tl + C::p_col + (tc & 1) * (KT / 2) + half * (HK / 2);
 #pragma unroll
-      for (int q = 0; q < HK / 32; ++q) {
-        uint32_t p[16];
+        for (int q = 0; q < HK / 32; ++q) {
+          uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
-          float x0, x1;
-          unpack2(x, x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          l2 = add2(l2, pack2(x0, x1));
-          p[i] = pack_f16(x0, x1);
+          for (int i = 0; i < 16; ++i) {
+            float s0 = __uint_as_float(s[32 * q + 2 * i]), s1 = __uint_as_float(s[32 * q + 2 * i + 1]);
+            if constexpr (decltype(rounded)::value) {  // (in scalars: a product and a sum of pairs are fused)
+              s0 = __fadd_rn(__fmul_rn(s0, fac), -m);
+              s1 = __fadd_rn(__fmul_rn(s1, fac), -m);
+            }
+            const uint64_t x = decltype(rounded)::value ? pack2(s0, s1) : fma2(pack2(s0, s1), fac2, nm2);
+            float x0, x1;
+            unpack2(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            l2 = add2(l2, pack2(x0, x1));
+            p[i] = pack_f16(x0, x1);
+          }
+          tmem_st16(tp + 16 * q, p);
         }
-        tmem_st16(tp + 16 * q, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[tc & 1]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[tc & 1]);
-    }
+    };
+    if (scores_far<D>(fac))
+      keys(std::true_type{});
+    else
+      keys(std::false_type{});
     // ---- the run's result
     next.get(a, walk, row, half);
     float l0, l1;
@@ -542,89 +545,90 @@ MOE_DEV void softmax_rows(const KvAttnArgs& a, TcShared& sh, Walk& walk, uint32_
     }
     // keys that every row of this half sees
     const int lim_min = a.causal ? max(sq.ctx - sq.n_q + first_row / a.G + 1, 0) : sq.ctx;
-    const bool far = scores_far<D>(fac);
-    const uint64_t fac2 = far ? pack2(1.0f, 1.0f) : pack2(fac, fac);
-    for (int j = 0; j < n; ++j, ++tc) {
-      ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[g], tc & 1, &sh.wait, a.status));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[KT];
+    const uint64_t fac2 = pack2(fac, fac);
+    auto keys = [&](auto rounded) {  // (two loops: a choice in one cost 1%)
+      for (int j = 0; j < n; ++j, ++tc) {
+        ok = __all_sync(0xffffffffu, wait_soon(&sh.s_full[g], tc & 1, &sh.wait, a.status));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[KT];
 #pragma unroll
-      for (int i = 0; i < KT; i += 32) tmem_ld32(tl + C::s_col + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_empty);
-      const int k0 = (run.u0 + j) * KT;
-      if (k0 + KT > lim_min) {
-        const int left = lim - k0;
+        for (int i = 0; i < KT; i += 32) tmem_ld32(tl + C::s_col + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_empty);
+        const int k0 = (run.u0 + j) * KT;
+        if (k0 + KT > lim_min) {
+          const int left = lim - k0;
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
-          if (i >= left) s[i] = 0xff800000u;
-      }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int i = 0; i < KT; ++i)
+            if (i >= left) s[i] = 0xff800000u;
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < KT; i += 2)
-        mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
-      if (__any_sync(0xffffffffu, mx - m > kLead + kRaise)) {
-        const float top = fmaxf(mx - kLead, m);
-        if (j > 0) {
-          const float fix = ex2(m - top);
-          float a0, a1;
-          unpack2(l2, a0, a1);
-          l2 = pack2(a0 * fix, a1 * fix);
-          ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
-          if (!ok) break;
-          tc_fence_after();
+        for (int i = 0; i < KT; i += 2)
+          mx4[(i / 2) & 3] = max3(mx4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
+        if (__any_sync(0xffffffffu, mx - m > kLead + kRaise)) {
+          const float top = fmaxf(mx - kLead, m);
+          if (j > 0) {
+            const float fix = ex2(m - top);
+            float a0, a1;
+            unpack2(l2, a0, a1);
+            l2 = pack2(a0 * fix, a1 * fix);
+            ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + c, o);
-            tmem_ld_wait();
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + c, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-            tmem_st16(to + c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+              tmem_st16(to + c, o);
+            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
+          m = top;
         }
-        m = top;
-      }
-      if (__builtin_expect(far, 0)) {
+        const uint64_t nm2 = pack2(-m, -m);
 #pragma unroll
-        for (int i = 0; i < KT; i += 2) {
-          float x0, x1;
-          unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack2(fac, fac)), x0, x1);
-          s[i] = __float_as_uint(x0);
-          s[i + 1] = __float_as_uint(x1);
-        }
-      }
-      const uint64_t nm2 = pack2(-m, -m);
+        for (int q = 0; q < KT / 32; ++q) {
+          uint32_t p[16];
 #pragma unroll
-      for (int q = 0; q < KT / 32; ++q) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t x = fma2(pack2(__uint_as_float(s[32 * q + 2 * i]), __uint_as_float(s[32 * q + 2 * i + 1])), fac2, nm2);
-          float x0, x1;
-          unpack2(x, x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          l2 = add2(l2, pack2(x0, x1));
-          p[i] = pack_f16(x0, x1);
+          for (int i = 0; i < 16; ++i) {
+            float s0 = __uint_as_float(s[32 * q + 2 * i]), s1 = __uint_as_float(s[32 * q + 2 * i + 1]);
+            if constexpr (decltype(rounded)::value) {  // (in scalars: a product and a sum of pairs are fused)
+              s0 = __fadd_rn(__fmul_rn(s0, fac), -m);
+              s1 = __fadd_rn(__fmul_rn(s1, fac), -m);
+            }
+            const uint64_t x = decltype(rounded)::value ? pack2(s0, s1) : fma2(pack2(s0, s1), fac2, nm2);
+            float x0, x1;
+            unpack2(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            l2 = add2(l2, pack2(x0, x1));
+            p[i] = pack_f16(x0, x1);
+          }
+          if (q == 0 && tc > 0) {  // the product that last read these columns
+            ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
+            tc_fence_after();
+          }
+          tmem_st16(tp + 16 * q, p);
         }
-        if (q == 0 && tc > 0) {  // the product that last read these columns
-          ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
-          tc_fence_after();
-        }
-        tmem_st16(tp + 16 * q, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&sh.p_full[g]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&sh.p_full[g]);
-    }
+    };
+    if (scores_far<D>(fac))
+      keys(std::true_type{});
+    else
+      keys(std::false_type{});
     if (!ok) break;
     next.get(a, walk, g * kHalf + row, 0);
     ok = __all_sync(0xffffffffu, wait_soon(&sh.pv_done[g], (tc - 1) & 1, &sh.wait, a.status));
