@@ -235,16 +235,22 @@ struct KvAttnArgs {
 };
 
 // Query rows per key head up to which the decode kernel takes a sequence. It reads the cache again
-// for every 16 rows; the tensor-core kernel takes 128 as fast as 1, but starts 10 us later. 16
-// sequences over 8192 keys, 32 + 8 heads, D = 128: decode 73, 126, 177, 229 us for 16, 32, 48, 64
-// rows, tensor cores 116 to 121; 16 + 2 heads, D = 256: decode 46, 71, 95, 120, tensor cores 66
-// to 68. (One sequence of 1000 keys alone: decode 17 to 20 us up to 64 rows, tensor cores 29.)
+// for every 16 rows; the tensor-core kernel takes 128 as fast as 1, but starts some 7 us later. 20 to 32
+// rows, decode and tensor cores in us: 32 + 8 heads of 128, 4 sequences over 4096 keys 26 and 33, 16
+// over 1024 33 and 38, 16 over 4096 70 and 67, 16 over 8192 122 and 108, 64 over 4096 246 and 199;
+// 16 + 2 heads of 256, 4 over 16384 37 and 40, 16 over 4096 41 and 39, 16 over 8192 62 and 55, 64 over
+// 4096 118 and 91; 14 + 2 heads of 64, 16 over 8192 31 and 38, 64 over 4096 54 and 60. So 32 suits
+// calls of up to some 60 us, and costs longer ones with heads of 128 and more up to a quarter; at 48
+// rows the decode kernel reads the cache three times (16 over 8192: 177 us, D = 256 95).
 constexpr int kDecMaxRows = 32;
 // A batch whose work is no more than this many of the decode kernel's units (64 keys for 16 rows) is
-// left to it whole, two launches instead of four. 32 + 8 heads, D = 128, decode alone against both:
-// 736 units (16 tokens over 1000 keys) 20 and 29 us, 1920 26 and 31, 4400 32 and 35, 5000 34 and 35,
-// 7200 48 and 33, 11200 60 and 38. 16 + 2 heads of 256: 850 units 22 and 29 us, 3200 34 and 35, 4256
-// 46 and 59, 4608 32 and 33, 7040 58 and 44.
+// left to it whole, two launches instead of four. Decode alone against both, in us: 32 + 8 heads of 128,
+// 920 units (16 tokens over 1000 keys) 15 and 23, 2520 20 and 22, 4224 27 and 28, 5632 26 and 30, 10280
+// (16 tokens over 16000) 37 and 32, 10560 (8 sequences of 40 tokens over 512) 46 and 31; 16 + 2 heads of
+// 256, 2160 units 16 and 23, 4788 (16 tokens over 16000) 37 and 53, 5214 40 and 35, 6144 34 and 30, 7056
+// 41 and 29; 14 + 2 heads of 64, 3552 units 21 and 24, 5888 25 and 23, 10672 37 and 26. The units are
+// what the host knows: the block table's width stands for the contexts, so a call with a wider table
+// than its contexts need takes both kernels sooner.
 constexpr int64_t kFewUnits = 4500;
 int64_t kv_attn_dec_units(int64_t T, int n_seqs, int G, int Hkv, int D, int64_t keys);  // at most
 size_t kv_attn_dec_part_floats(int D);

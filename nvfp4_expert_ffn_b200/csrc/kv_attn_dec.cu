@@ -17,10 +17,13 @@
 //     interleaved nibble by nibble first (a quarter of an instruction per element); the scores'
 //     fragments turn into P^T operands with movmatrix. Row r of a tile is key key_of(r), which
 //     makes a thread's four keys of V four rows apart: a warp reads four whole rows at a time.
-// What bounds it now is still those instructions: 384 a warp for 16 keys of 128 elements, 0.61 a
-// cycle, the integer pipe (which converts the codes) 55% busy. One B200: 64 sequences over up to
-// 8192 keys, 32 + 8 heads of 128, 99 us (3.7 TB/s); 8 sequences near 16384 keys, 16 + 2 heads of
-// 256, 30 us; one over 1000 keys 12.7 us.
+// What bounds it now is those instructions and the chain they make: 384 a warp for 16 keys of 128
+// elements, from the codes to the products of P and V each waiting for the one before; 61% of the issue
+// slots are used, the integer pipe (which converts the codes) is 55% busy, and 4 warps a scheduler do
+// not cover the rest. One B200: 64 sequences over up to 8192 keys, 32 + 8 heads of 128, 100 us (3.6
+// TB/s), 14 + 2 heads of 64 26.6 us (1.7 TB/s); 8 sequences near 16384 keys, 16 + 2 heads of 256, 31 us;
+// one over 1000 keys 12.8 us. (With heads of 256 some registers are spilled: 92 bytes a thread by 8
+// rows, 244 by 16.)
 // q is scaled by a power of two per row into float16's range (exact; the factor returns in
 // the softmax scale), the weights P are rounded to float16 (11 bits; the result is bf16, 8; see kLead),
 // sums, maxima and the output stay in float32.

@@ -19,11 +19,12 @@
 //   both P fill TMEM, so Q is in shared memory. Bound by the softmax warps' instructions and the
 //   exponentials (256 x 128 scores in 3400 cycles, the products alone 2450). One group of 128 rows
 //   a block with two threads a row took 2430 cycles for half as many: 27140 tokens in chunks over
-//   caches up to 16K (32 + 8 heads, D = 128) 3350 us, now 2275 us (1220 TFLOP/s; 2640 us in a row
-//   with itself, under the power limit).
+//   caches up to 16K (32 + 8 heads, D = 128) 3350 us, now 2280 us (1220 TFLOP/s; 2650 us in a row
+//   with itself, under the power limit). A prompt of 16384, 14 + 2 heads of 64, 734 us (655 TFLOP/s:
+//   half the products for the same exponentials).
 // D = 256: O, Q and S of 128 rows leave no columns for a second group or more than KT = 64 keys,
 //   at which a Q K^T costs as much as at 128; bound by the products (1536 cycles of 1750 a tile).
-//   A prompt of 16384 (16 + 2 heads) 2040 us (1080 TFLOP/s), 2270 us in a row with itself.
+//   A prompt of 16384 (16 + 2 heads) 2045 us (1075 TFLOP/s), 2280 us in a row with itself.
 // The loops are kept short where that costs nothing: the roles' code together passes the
 // instruction cache (an expander unrolled 16 times instead of 4 made the softmax 12% slower).
 //

@@ -12,10 +12,12 @@
 // by up to half of itself. Queries end in bf16 and are float32.
 //
 // Per token Hq + 2 Hkv rows of 2D bytes are read, Hq rows written, 9/16 byte a cached element: for
-// many tokens HBM's bytes would bound it, but the instructions do (issue slots 69% used). One B200:
-// norm and rotation of 16384 tokens (32 + 8 heads of 128) 77 to 80 us, 4.3 TB/s; with the write of keys
-// and values, and those read back, 27140 tokens 200 us, 3.6 TB/s. For a few tokens the launch and the float64 sine and
-// cosine: 4.1 us for 8 tokens (16 + 2 heads of 256), 7.4 us with the write and the read back.
+// many tokens HBM's bytes would bound it. Nothing is full: issue slots 73 to 74%, 7 of 16 warps a scheduler
+// (64 registers a thread, and the tables' shared memory), which wait for dependent instructions, shared
+// memory and loads in about equal parts. One B200: norm and rotation of 16384 tokens (32 + 8 heads of
+// 128) 78 to 80 us, 4.3 TB/s; with the write of keys and values, and those read back, 27140 tokens 199 us,
+// 3.7 TB/s. For a few tokens the launch and the float64 sine and cosine: 4.1 us for 8 tokens (16 + 2 heads
+// of 256), 7.4 us with the write and the read back.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -388,8 +390,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) qkv_prep_kernel(const QkvPr
 // 8 elements a thread and output: 4 bytes of codes and the block's scale -> one 16-byte store
 // (bf16) or two (float32), of the key and the value at once. A thread keeps its head and place
 // and walks over the rows, four at a time, so that their loads are under way together, and reads the
-// slots of the next four before (6 us less). Bound by
-// the bytes written: 65536 rows of 2 heads of 256 as bf16, 34 us (5.0 TB/s, launch included).
+// slots of the next four before (6 us less). Bound by the bytes written: 65536 rows of 2 heads of 256
+// as bf16, 33.5 us (5.1 TB/s, launch included), as float32 81 us (3.8 TB/s).
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheArgs c, int page_shift, const int32_t* slots,
                                                       int64_t n, void* k_out, void* v_out,
